@@ -309,6 +309,97 @@ int hs2_sparse_decode_workspace(const hs2_shape* shape, int32_t n, size_t* works
 int hs2_swa_attn(const hs2_shape* shape, const void* q, const void* k, const void* v, int32_t window, void* o,
                  float* lse, void* stream);
 
+/* ---- serving around a paged K/V cache ---- */
+
+/*
+ * A K/V cache of several sequences, in pages of `page` consecutive tokens.
+ * k and v are pools [n_pages * page][Hkv][d] (bf16, or e4m3 codes with fp32
+ * scales [n_pages * page][Hkv], as in hs2_shape); position p of sequence b
+ * is token page_table[b][p / page] * page + p % page of the pools.  A batch-1
+ * cache as the prefill calls use it is such a pool, its pages numbered in
+ * order.  The struct holds device pointers and sizes only; the library keeps
+ * nothing of it.
+ *
+ * Supported: d = 128, page in {16, 32, 64, 128}, 1 <= n_seqs <= 4096,
+ * 1 <= Hkv <= 256, n_pages * page <= 2^31 - 256, max_pages * page <= 2^30;
+ * pools 16-byte aligned, strides multiples of 8 elements (16 for e4m3) with
+ * rows that do not overlap.  Else HS2_ERR_UNSUPPORTED.
+ */
+typedef struct hs2_cache {
+  int32_t Hkv, d, kv_dtype;
+  int32_t page, n_pages;      /* tokens per page, pages in the pools */
+  int32_t n_seqs, max_pages;  /* page_table is int32 [n_seqs][max_pages] */
+  int32_t reserved;           /* 0 */
+  int64_t tok_stride, head_stride; /* elements of k and v */
+  void *k, *v;
+  float *k_scale, *v_scale;   /* e4m3 only */
+  const int32_t* page_table;  /* may be NULL where a call does not read it */
+} hs2_cache;
+
+/*
+ * n new tokens' query, key and value rows (views of one projection's output,
+ * say): q bf16 [n][Hq][d] with the q strides, k and v bf16 [n][Hkv][d] with
+ * the kv strides, the rotated queries written with the out strides.
+ */
+typedef struct hs2_rope {
+  int32_t n, Hq;
+  int32_t rot;          /* rotated leading dimensions of a head: 16, 32, ..., 128 */
+  int32_t interleaved;  /* 0: pairs (f, f + rot / 2); 1: pairs (2f, 2f + 1) */
+  float eps;
+  int32_t reserved;     /* 0 */
+  int64_t q_tok_stride, q_head_stride, kv_tok_stride, kv_head_stride, out_tok_stride, out_head_stride;
+} hs2_rope;
+
+/*
+ * Norms of queries and keys per head with the position rotation, and the
+ * cache write, in one pass (the step before every attention call here).  For
+ * a query or key row x of 128 values at position t:
+ *   y_i = x_i / sqrt(mean_i x_i^2 + eps) * w_i        (w NULL: y = x)
+ *   (y_a, y_b) -> (y_a cos u - y_b sin u, y_b cos u + y_a sin u),
+ *   u = t * inv_freq[f],
+ * over the rot / 2 pairs (a, b) of the layout above; dimensions rot .. 127
+ * are not rotated.  u is reduced in 64 bits, so far positions lose nothing;
+ * all else is fp32, rounded once.  Query r goes to q_out[r]; the key (rotated)
+ * and the value (unchanged) go to token slots[r] of the cache's pools (NULL:
+ * token r), as bf16 or as e4m3 codes with scale = amax / 448 of the fp32 row
+ * (1 for a row of zeros), the format hs2_quantize_kv writes.  slots[r] = -1
+ * leaves the cache alone for that row; any other slot outside
+ * [0, n_pages * page) is reported by hs2_sync as HS2_ERR_INDEX and skipped.
+ * The slots of one call must be distinct.
+ *
+ * q_weight, k_weight: bf16 [128], both NULL or both given.  inv_freq: double
+ * [rot / 2].  positions: int32 [n].  slots: int32 [n] or NULL.  q_out may be
+ * q (same strides), and nothing else may overlap an input.  n = 0 does nothing.
+ * page_table, n_seqs and max_pages of the cache are not read.  Device
+ * pointers; asynchronous on `stream`.
+ */
+int hs2_qk_norm_rope(const hs2_cache* cache, const hs2_rope* rope, const void* q, const void* k, const void* v,
+                     const void* q_weight, const void* k_weight, const double* inv_freq, const int32_t* positions,
+                     const int32_t* slots, void* q_out, void* stream);
+
+/*
+ * Eviction by collected weight.  A sequence b of n = seq_len[b] > keep tokens
+ * keeps, for each KV head on its own, the keep - recent positions of
+ * [0, n - recent) with the largest acc (ties to the lower position) and the
+ * last `recent`; in ascending order they become positions 0 .. keep - 1:
+ * their K and V rows (and scales) are moved inside the sequence's own pages,
+ * in place, and their acc is written to acc_out[b][g][0 .. keep), followed by
+ * zeros up to n.  What lies at positions keep .. n - 1 of the cache stays as
+ * it was (those pages can be freed).  A sequence of at most keep tokens stays
+ * as it is.  idx[b][g][i] (int32 [n_seqs][Hkv][keep]) is the old position of
+ * the new position i, -1 padded; new_len[b] = min(n, keep).
+ *
+ * acc fp32 [n_seqs][Hkv][acc_stride], finite values; acc_out the same layout,
+ * may be acc itself or NULL (not wanted), but not overlap it otherwise.
+ * new_len must not be seq_len.  0 <= recent <= keep, 1 <= keep <= 2^24.
+ * No page of the table may appear twice among the sequences' pages in use.
+ * A length outside [0, max_pages * page] or above acc_stride, or a page
+ * outside the pools, is reported by hs2_sync as HS2_ERR_INDEX; such a
+ * sequence is skipped, such a page's rows are not moved.
+ */
+int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float* acc, float* acc_out,
+                    int64_t acc_stride, int32_t keep, int32_t recent, int32_t* idx, int32_t* new_len, void* stream);
+
 /* ---- diagnostics ---- */
 
 /* Short text for an hs2_status code (static storage). */

@@ -944,3 +944,5 @@ int hs2_sync(void* stream) {
 }
 
 }  // extern "C"
+
+#include "serving.cuh"

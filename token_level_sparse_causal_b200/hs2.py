@@ -24,7 +24,7 @@ EXPORTS = ("hs2_full_attn_select", "hs2_sparse_attn", "hs2_sync", "hs2_attn_fwd"
            "hs2_topk_select", "hs2_strerror", "hs2_debug_set", "hs2_version", "hs2_launch_count",
            "hs2_full_attn_select_static", "hs2_exp2_check", "hs2_quantize_kv", "hs2_block_select",
            "hs2_full_attn_select_blocks", "hs2_swa_attn", "hs2_sparse_decode",
-           "hs2_sparse_decode_workspace", "hs2_attn_fwd_ws")
+           "hs2_sparse_decode_workspace", "hs2_attn_fwd_ws", "hs2_qk_norm_rope", "hs2_cache_evict")
 
 
 class Hs2Shape(ctypes.Structure):
@@ -32,6 +32,23 @@ class Hs2Shape(ctypes.Structure):
                 ("block", ctypes.c_int32), ("topk", ctypes.c_int32), ("recent", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
                 ("kv_tok_stride", ctypes.c_int64), ("kv_head_stride", ctypes.c_int64)]
+
+
+class Hs2Cache(ctypes.Structure):
+    """hs2_cache: a paged K/V cache (make_cache builds it and keeps its tensors alive)."""
+    _fields_ = [("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("reserved", ctypes.c_int32), ("tok_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class Hs2Rope(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("Hq", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("kv_tok_stride", ctypes.c_int64), ("kv_head_stride", ctypes.c_int64),
+                ("out_tok_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
 
 
 class Hs2Error(RuntimeError):
@@ -65,6 +82,9 @@ _SIGS = {
     "hs2_exp2_check": [_vp, _vp, _vp, _vp, _i64, _vp],
     "hs2_quantize_kv": [_i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp],
     "hs2_version": [],
+    "hs2_qk_norm_rope": [ctypes.POINTER(Hs2Cache), ctypes.POINTER(Hs2Rope), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                         _vp, _vp],
+    "hs2_cache_evict": [ctypes.POINTER(Hs2Cache), _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp],
 }
 
 
@@ -239,6 +259,109 @@ def hs2_launch_count() -> int:
 def hs2_exp2_check(x, y_mufu, y_fma3, y_fma4, stream=None) -> None:
     _check(lib().hs2_exp2_check(_ptr(x), _ptr(y_mufu), _ptr(y_fma3), _ptr(y_fma4), x.numel(), _stream(stream)),
            "hs2_exp2_check")
+
+
+# --------------------------------------------- serving around a paged cache --
+
+def _need(t: Optional[torch.Tensor], dtype, shape, what: str, contiguous: bool = True, like=None) -> None:
+    """Argument check of a device tensor; shape entries of None are free."""
+    if t is None:
+        return
+    ok = t.dtype in (dtype if isinstance(dtype, tuple) else (dtype,)) and t.dim() == len(shape)
+    if not ok or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise ValueError(f"{what}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    if not contiguous and t.shape[-1] != 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{what}: on {t.device}, expected {like.device}")
+
+
+def _strides(t: torch.Tensor) -> tuple:
+    """Token and head stride of a [tokens][H][d] tensor, with the packed value for a dimension of size 1 (whose
+    stride torch leaves open)."""
+    n, H, d = t.shape
+    head = t.stride(1) if H > 1 else d
+    return (t.stride(0) if n > 1 else H * head), head
+
+
+def _call(name: str, device: torch.device, stream, *args) -> None:
+    """Call a library function whose last argument is the stream, on `device`
+    (its current stream unless one is given)."""
+    fn = getattr(lib(), name)
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), name)
+    else:
+        _check(fn(*args, _stream(stream)), name)
+
+
+def make_cache(k, v, page_table, page: int, k_scale=None, v_scale=None) -> Hs2Cache:
+    """hs2_cache over the pools k, v [n_pages * page][Hkv][128] (bf16; uint8 or
+    float8_e4m3fn with fp32 scales [n_pages * page][Hkv]) and an int32 page
+    table [n_seqs][max_pages] (None where only hs2_qk_norm_rope uses it)."""
+    f8 = k.dtype in (torch.uint8, torch.float8_e4m3fn)
+    _need(k, (torch.uint8, torch.float8_e4m3fn) if f8 else torch.bfloat16, (None, None, 128), "k", contiguous=False)
+    _need(v, k.dtype, tuple(k.shape), "v", contiguous=False, like=k)
+    if _strides(v) != _strides(k):
+        raise ValueError("v: must have k's strides")
+    if page <= 0 or k.shape[0] % page:
+        raise ValueError(f"page: {page} does not divide the pools' {k.shape[0]} tokens")
+    if f8 != (k_scale is not None) or f8 != (v_scale is not None):
+        raise ValueError("k_scale, v_scale: given exactly with an e4m3 cache")
+    _need(k_scale, torch.float32, (k.shape[0], k.shape[1]), "k_scale", like=k)
+    _need(v_scale, torch.float32, (k.shape[0], k.shape[1]), "v_scale", like=k)
+    _need(page_table, torch.int32, (None, None), "page_table", like=k)
+    n_seqs, max_pages = (0, 0) if page_table is None else page_table.shape
+    ptr = lambda t: None if t is None else t.data_ptr()
+    c = Hs2Cache(Hkv=k.shape[1], d=k.shape[2], kv_dtype=HS2_KV_E4M3 if f8 else HS2_KV_BF16, page=page,
+                 n_pages=k.shape[0] // page, n_seqs=n_seqs, max_pages=max_pages, tok_stride=_strides(k)[0],
+                 head_stride=_strides(k)[1], k=ptr(k), v=ptr(v), k_scale=ptr(k_scale), v_scale=ptr(v_scale),
+                 page_table=ptr(page_table))
+    c.tensors = (k, v, page_table, k_scale, v_scale)
+    return c
+
+
+def hs2_qk_norm_rope(cache: Hs2Cache, q, k, v, q_weight, k_weight, eps: float, inv_freq, positions, slots, q_out,
+                     interleaved: bool = False, stream=None) -> None:
+    """q, q_out [n][Hq][128], k, v [n][Hkv][128] bf16 (any token and head strides), inv_freq float64 [rot / 2],
+    positions and slots int32 [n] (slots None: rows 0 .. n - 1 of the pools; -1: no cache write)."""
+    n, Hq, _ = q.shape
+    pool = cache.tensors[0]
+    _need(q, torch.bfloat16, (n, Hq, 128), "q", False, pool)
+    _need(q_out, torch.bfloat16, (n, Hq, 128), "q_out", False, pool)
+    _need(k, torch.bfloat16, (n, cache.Hkv, 128), "k", False, pool)
+    _need(v, torch.bfloat16, (n, cache.Hkv, 128), "v", False, pool)
+    if _strides(v) != _strides(k):
+        raise ValueError("v: must have k's strides")
+    _need(q_weight, torch.bfloat16, (128,), "q_weight", True, pool)
+    _need(k_weight, torch.bfloat16, (128,), "k_weight", True, pool)
+    _need(inv_freq, torch.float64, (None,), "inv_freq", True, pool)
+    _need(positions, torch.int32, (n,), "positions", True, pool)
+    _need(slots, torch.int32, (n,), "slots", True, pool)
+    if slots is None and n > pool.shape[0]:
+        raise ValueError(f"slots: {n} rows do not fit the pools' {pool.shape[0]} tokens")
+    r = Hs2Rope(n, Hq, 2 * inv_freq.numel(), int(interleaved), eps, 0, *_strides(q), *_strides(k),
+                *_strides(q_out))
+    _call("hs2_qk_norm_rope", pool.device, stream, ctypes.byref(cache), ctypes.byref(r), _ptr(q), _ptr(k), _ptr(v),
+          _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(slots), _ptr(q_out))
+
+
+def hs2_cache_evict(cache: Hs2Cache, seq_len, acc, keep: int, recent: int, idx, new_len, acc_out=None,
+                    stream=None) -> None:
+    """seq_len, new_len int32 [n_seqs]; acc (and acc_out, which may be acc) fp32 [n_seqs][Hkv][acc_stride];
+    idx int32 [n_seqs][Hkv][keep]."""
+    pool, B = cache.tensors[0], cache.n_seqs
+    _need(seq_len, torch.int32, (B,), "seq_len", True, pool)
+    _need(new_len, torch.int32, (B,), "new_len", True, pool)
+    _need(acc, torch.float32, (B, cache.Hkv, None), "acc", True, pool)
+    _need(acc_out, torch.float32, tuple(acc.shape), "acc_out", True, pool)
+    _need(idx, torch.int32, (B, cache.Hkv, keep), "idx", True, pool)
+    _call("hs2_cache_evict", pool.device, stream, ctypes.byref(cache), _ptr(seq_len), _ptr(acc), _ptr(acc_out),
+          acc.shape[2], int(keep), int(recent), _ptr(idx), _ptr(new_len))
 
 
 # hs2_debug_set flag bits (include/hs2.h)
