@@ -378,6 +378,97 @@ int hs2_qk_norm_rope(const hs2_cache* cache, const hs2_rope* rope, const void* q
                      const int32_t* slots, void* q_out, void* stream);
 
 /*
+ * Packed prompts: sequence b's queries are tokens [cu_q[b], cu_q[b + 1]) of q
+ * and o, its keys and values tokens [cu_k[b], cu_k[b + 1]) of k and v.
+ * total_q, total_k are the tokens these buffers hold; what lies behind the
+ * last sequence is not read into a result and not written.  Hq / Hkv is any
+ * whole number up to 16; lengths are any, 0 included.  q and o share strides,
+ * k and v too.  1 <= n_seqs <= 4096; strides multiples of 8, bases 16-byte
+ * aligned.
+ */
+typedef struct hs2_varlen {
+  int32_t n_seqs, total_q, total_k;
+  int32_t Hq, Hkv, d;
+  int64_t q_tok_stride, q_head_stride;
+  int64_t kv_tok_stride, kv_head_stride;
+} hs2_varlen;
+
+/*
+ * Causal grouped-query attention over packed prompts of different lengths
+ * (kernel 1's attention without its one-sequence, multiple-of-64 shape):
+ * query i of a sequence with nq queries and nk keys sees its keys
+ * j <= i + nk - nq, so nk > nq continues a prompt whose first nk - nq keys
+ * are there already.  o = softmax(q.k / sqrt(d)) v, lse (fp32 [Hq][total_q],
+ * optional) its natural-log sum.  A query that sees no key (nk < nq) gets
+ * zeros and -inf.
+ *
+ * cu_q, cu_k: int32 [n_seqs + 1] on the device, ascending; cu_k NULL: equal
+ * to cu_q.  Entries that descend or leave [0, total] are reported by hs2_sync
+ * as HS2_ERR_INDEX, and the call then writes nothing.  The values of a
+ * sequence's own tokens have to be finite; tokens outside the sequences may
+ * hold anything.  Asynchronous on `stream`.
+ */
+int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const void* v, const int32_t* cu_q,
+                    const int32_t* cu_k, void* o, float* lse, void* stream);
+
+/*
+ * Drafted tokens of a batch: sequence b has ctx_len[b] committed tokens in
+ * the cache and T_b = cu_draft[b + 1] - cu_draft[b] drafted ones (0 .. 64)
+ * right behind them, at positions ctx_len[b] .. ctx_len[b] + T_b - 1, whose
+ * queries are rows cu_draft[b] .. of q.  Row r of sequence b sees every
+ * committed token, and drafted token j of its sequence iff bit j of mask[r]
+ * is set (bits >= T_b are ignored; its own bit is not implied); mask NULL:
+ * the drafted tokens are a chain, each seeing itself and those before it.
+ * T_b = 1 without a mask is ordinary decoding.
+ *
+ * max_draft: at least every T_b, 1 .. 64.  Hq / Hkv any whole number up to
+ * 16.  A sequence whose lengths are negative, above max_draft or above
+ * max_pages * page, rows outside [0, n_tok], or a page outside the pools are
+ * reported by hs2_sync as HS2_ERR_INDEX; such a sequence (or such an array
+ * cu_draft) is skipped, such a page reads as zeros.
+ */
+typedef struct hs2_draft {
+  int32_t n_tok, max_draft, Hq, reserved; /* reserved: 0 */
+  int64_t q_tok_stride, q_head_stride;    /* elements of q and o */
+  const int32_t* cu_draft;                /* [n_seqs + 1] */
+  const int32_t* ctx_len;                 /* [n_seqs] */
+  const uint64_t* mask;                   /* [n_tok] or NULL */
+} hs2_draft;
+
+/*
+ * Attention of drafted tokens over the paged cache: q, o bf16 [n_tok][Hq][d],
+ * lse fp32 [Hq][n_tok] (optional, natural log).  A row that sees nothing gets
+ * zeros and -inf.  Values of tokens inside a sequence (committed or drafted)
+ * have to be finite, those behind it in its last page may be anything.
+ * Rows of q and o outside [cu_draft[0], cu_draft[n_seqs]) are left alone.
+ * n_tok = 0 does nothing.
+ *
+ * workspace: hs2_tree_attn_workspace(cache, draft) bytes, 16-byte aligned; it
+ * holds no state between calls, but two calls in flight at once (two graphs
+ * that may replay together, too) must not share it.
+ */
+int hs2_tree_attn(const hs2_cache* cache, const hs2_draft* draft, const void* q, void* o, float* lse,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace size in bytes hs2_tree_attn needs; host only. */
+int hs2_tree_attn_workspace(const hs2_cache* cache, const hs2_draft* draft, size_t* workspace_bytes);
+
+/*
+ * The weight that cached tokens collect: for sequence b, KV head g, position
+ * j < ctx_len[b] + T_b,
+ *   acc[b][g][j] += sum over the counted rows r of b that see j and the heads
+ *                   h of g of exp(q_rh . k_j / sqrt(d) - lse[h][r]),
+ * with the lse that hs2_tree_attn gave for the same rows.  counted: uint8
+ * [n_tok], rows with 0 are left out (drafted tokens that were not accepted);
+ * NULL counts all.  Rows with lse = -inf collect nothing.  acc: fp32
+ * [n_seqs][Hkv][acc_stride]; acc_stride a multiple of 4 and at least every
+ * length.  Positions behind a sequence are not touched.  The sums are added in
+ * a fixed order; two calls on one acc must not run at once.
+ */
+int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void* q, const float* lse,
+                      const uint8_t* counted, float* acc, int64_t acc_stride, void* stream);
+
+/*
  * Eviction by collected weight.  A sequence b of n = seq_len[b] > keep tokens
  * keeps, for each KV head on its own, the keep - recent positions of
  * [0, n - recent) with the largest acc (ties to the lower position) and the

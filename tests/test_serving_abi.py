@@ -56,15 +56,102 @@ def evict_call(lib, c, lens=P, acc=P, acc_out=P + 64, stride=256, keep=32, recen
                                ST)
 
 
+def draft(**kw):
+    base = dict(n_tok=6, max_draft=4, Hq=8, reserved=0, q_tok_stride=1024, q_head_stride=128, cu_draft=P, ctx_len=P,
+                mask=P)
+    base.update(kw)
+    return hs2.Hs2Draft(**base)
+
+
+def tree_call(lib, c, d=None, q=P, o=P + 64, lse=P, ws=P, wsb=1 << 30):
+    return lib.hs2_tree_attn(ctypes.byref(c), ctypes.byref(d or draft()), vp(q), vp(o), vp(lse), vp(ws), wsb, ST)
+
+
+def weights_call(lib, c, d=None, q=P, lse=P, counted=P, acc=P, stride=256):
+    return lib.hs2_cache_weights(ctypes.byref(c), ctypes.byref(d or draft()), vp(q), vp(lse), vp(counted), vp(acc),
+                                 stride, ST)
+
+
+def varlen_call(lib, q=P, k=P, v=P, cu_q=P, cu_k=P, o=P + 64, lse=P, **kw):
+    base = dict(n_seqs=3, total_q=100, total_k=100, Hq=8, Hkv=2, d=128, q_tok_stride=1024, q_head_stride=128,
+                kv_tok_stride=256, kv_head_stride=128)
+    base.update(kw)
+    s = hs2.Hs2Varlen(**base)
+    return lib.hs2_varlen_attn(ctypes.byref(s), vp(q), vp(k), vp(v), vp(cu_q), vp(cu_k), vp(o), vp(lse), ST)
+
+
 @pytest.mark.parametrize("kw,code", BAD_CACHES)
 def test_bad_caches(lib, kw, code):
-    assert rope_call(lib, cache(**kw)) == code
-    assert evict_call(lib, cache(**kw)) == code
+    n = ctypes.c_size_t(0)
+    for call in (rope_call, evict_call, tree_call, weights_call):
+        assert call(lib, cache(**kw)) == code
+    assert lib.hs2_tree_attn_workspace(ctypes.byref(cache(**kw)), ctypes.byref(draft()), ctypes.byref(n)) == code
 
 
 @pytest.mark.parametrize("kw,code", BAD_TABLES)
 def test_bad_tables(lib, kw, code):
-    assert evict_call(lib, cache(**kw)) == code
+    for call in (evict_call, tree_call, weights_call):
+        assert call(lib, cache(**kw)) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_tok=-1), INV), (dict(max_draft=0), INV), (dict(max_draft=65), INV), (dict(Hq=7), INV), (dict(Hq=0), INV),
+    (dict(Hq=34, q_tok_stride=34 * 128), UNS), (dict(reserved=1), INV), (dict(cu_draft=None), INV),
+    (dict(ctx_len=None), INV), (dict(q_tok_stride=1000), UNS), (dict(q_tok_stride=512), UNS),
+    (dict(q_head_stride=0), INV), (dict(cu_draft=P + 2), UNS), (dict(ctx_len=P + 1), UNS), (dict(mask=P + 4), UNS),
+])
+def test_bad_drafts(lib, kw, code):
+    n = ctypes.c_size_t(0)
+    assert tree_call(lib, cache(), draft(**kw)) == code
+    assert weights_call(lib, cache(), draft(**kw)) == code
+    assert lib.hs2_tree_attn_workspace(ctypes.byref(cache()), ctypes.byref(draft(**kw)), ctypes.byref(n)) == code
+
+
+def test_tree_attn_arguments(lib):
+    n = ctypes.c_size_t(0)
+    c, d = ctypes.byref(cache()), ctypes.byref(draft())
+    assert lib.hs2_tree_attn_workspace(c, d, ctypes.byref(n)) == hs2.HS2_OK and n.value > 0
+    assert lib.hs2_tree_attn_workspace(c, d, None) == INV
+    for kw, code in ((dict(q=None), INV), (dict(o=None), INV), (dict(ws=None), INV), (dict(wsb=n.value - 1), WSP),
+                     (dict(q=MIS), UNS), (dict(o=MIS), UNS), (dict(ws=MIS), UNS), (dict(lse=P + 2), UNS)):
+        assert tree_call(lib, cache(), **kw) == code
+    assert tree_call(lib, cache(), draft(n_tok=0), q=None, o=None, ws=None) == hs2.HS2_OK
+
+
+def test_cache_weights_arguments(lib):
+    for kw, code in ((dict(q=None), INV), (dict(lse=None), INV), (dict(acc=None), INV), (dict(stride=0), INV),
+                     (dict(stride=255), INV), (dict(q=MIS), UNS), (dict(acc=MIS), UNS), (dict(lse=P + 2), UNS)):
+        assert weights_call(lib, cache(), **kw) == code
+    assert weights_call(lib, cache(), draft(n_tok=0), q=None, lse=None, acc=None) == hs2.HS2_OK
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_seqs=0), INV), (dict(n_seqs=4097), UNS), (dict(total_q=-1), INV), (dict(total_k=-1), INV),
+    (dict(Hq=9), INV), (dict(Hkv=0), INV), (dict(Hq=34, q_tok_stride=34 * 128), UNS), (dict(d=64), UNS),
+    (dict(q_tok_stride=1004), UNS), (dict(q_tok_stride=512), UNS), (dict(kv_head_stride=64), UNS),
+    (dict(kv_tok_stride=-256), INV), (dict(cu_q=None), INV), (dict(q=None), INV), (dict(k=None), INV),
+    (dict(v=None), INV), (dict(o=None), INV), (dict(q=MIS), UNS), (dict(k=MIS), UNS), (dict(o=MIS), UNS),
+    (dict(lse=P + 1), UNS), (dict(cu_q=P + 2), UNS), (dict(cu_k=P + 2), UNS),
+    (dict(total_q=(1 << 31) - 1, Hq=2048, Hkv=128, q_tok_stride=2048 * 128, kv_tok_stride=128 * 128), UNS),
+])
+def test_bad_packed_prompts(lib, kw, code):
+    assert varlen_call(lib, **kw) == code
+
+
+def test_no_queries_is_no_work(lib):
+    assert varlen_call(lib, total_q=0, q=None, o=None) == hs2.HS2_OK
+
+
+def test_a_failing_tensor_map_launches_nothing(lib):
+    """The host-side fault injection of hs2_debug_set covers every call that encodes a descriptor."""
+    assert lib.hs2_debug_set(2_000_000_000, hs2.DEBUG_FAIL_TMAP) == hs2.HS2_OK
+    try:
+        before = hs2.hs2_launch_count()
+        for rc in (tree_call(lib, cache()), weights_call(lib, cache()), varlen_call(lib)):
+            assert rc == hs2.HS2_ERR_CUDA
+        assert hs2.hs2_launch_count() == before
+    finally:
+        lib.hs2_debug_set(2_000_000_000, 0)
 
 
 @pytest.mark.parametrize("kw,code", [

@@ -1,0 +1,418 @@
+// The attention weight that cached tokens collect from drafted queries:
+//   acc[b][g][j] += sum over counted rows r and heads h of g of
+//                   exp(q_rh . k_j / sqrt(d) - lse[h][r])   (0 where j is masked)
+//
+// As kernel (2) (importance.cuh) the keys lie on the MMA's M dimension: D =
+// K tile (128 keys x d) * Q^T (d x up to 128 query rows), so TMEM lane r holds
+// key r against every row and the thread that owns it adds its row up in
+// registers, with no reduction between threads and no atomics: each position
+// is written by one thread, in a fixed order.
+//
+// K is read once (256 B a key and KV head, 132 B as e4m3).  Work is split as
+// in tree_attn.cuh, but by (sequence, KV head): a CTA takes an equal stretch of
+// all key tiles, and for more than 128 rows walks its part of a sequence once
+// per 128 rows (adding to what it wrote; the K tiles then come from L2).  Two
+// epilogue warpgroups take the even and the odd tiles; bound by memory up to
+// about 100 rows, then by the exponentials (one per row and key, 16 a clock
+// and SM).  Exponentials run on the MUFU unit (2^-22): the cubic polynomial
+// that kernel (2) mixes in is exact only to 7.5e-5.
+//
+// e4m3: codes arrive by TMA in a raw ring and are turned into bf16 by four
+// warps; the key's scale multiplies its row of scores.
+#pragma once
+
+#include "tree_attn.cuh"
+
+namespace hs2 {
+
+constexpr int CW_ITEMS = 5;      // bf16: K tiles in the ring
+constexpr int CW_ITEMS_KV8 = 3;  // e4m3: converted tiles
+constexpr int CW_RAW = 5;        // e4m3: raw tiles
+
+struct WeightParams {
+  TreeParams t;          // geometry, table, cu, ctx, mask, scales, limits
+  const float* lse;      // [Hq][n_tok]
+  const uint8_t* counted;
+  float* acc;            // [B][Hkv][acc_stride]
+  int64_t acc_stride;
+};
+
+struct WeightBars {
+  uint64_t full[CW_ITEMS], empty[CW_ITEMS];
+  uint64_t raw_full[CW_RAW], raw_empty[CW_RAW];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], s_empty[2];
+  uint64_t rows_ready[2];
+  uint64_t fin;
+  int64_t first, count;
+  int b, g, tile;
+  uint32_t tmem_slot;
+  int abort;
+};
+static_assert(sizeof(WeightBars) <= 512, "barrier area");
+
+template <bool KV8>
+struct WeightSmem {
+  static constexpr int ITEMS = KV8 ? CW_ITEMS_KV8 : CW_ITEMS;
+  static constexpr uint32_t ITEM = TILE_BYTES;  // after Q
+  static constexpr uint32_t RAW = ITEM + ITEMS * TILE_BYTES;
+  static constexpr uint32_t BAR = RAW + (KV8 ? CW_RAW * RAW_BYTES : 0u);
+  // per epilogue warpgroup and segment parity, for each column (query row):
+  static constexpr uint32_t BITS = BAR + 512u;            // uint64 [2][2][128]: the drafted keys it sees
+  static constexpr uint32_t NLSE = BITS + 2 * 2 * 1024u;  // float [2][2][128]: -lse * log2(e); -inf: collects nothing
+  static constexpr uint32_t BYTES = NLSE + 2 * 2 * 512u;
+  static_assert(BYTES <= 232448u, "shared memory of one CTA");
+};
+
+// Walks one CTA's stretch: segments are (sequence, KV head, key tiles t0 .. t1,
+// token tile m); all token tiles of a key range come one after another.
+struct WeightWalk {
+  int b, g, m, row0, T, ctx, tiles, mtiles, t0, t1;
+  int64_t left;
+  __device__ __forceinline__ void load(const TreeParams& p) {
+    tree_seq(p, b, row0, T, ctx);
+    tiles = T ? (ctx + T + 127) >> 7 : 0;
+    mtiles = (T + p.R - 1) / p.R;
+  }
+  __device__ __forceinline__ bool begin(const TreeParams& p, const WeightBars* bars) {
+    left = bars->count;
+    if (left <= 0) return false;
+    b = bars->b;
+    g = bars->g;
+    m = 0;
+    load(p);
+    t0 = bars->tile;
+    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + left));
+    return true;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    if (++m < mtiles) return true;
+    m = 0;
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    if (++g == p.Hkv) {
+      g = 0;
+      do {
+        ++b;
+        load(p);
+      } while (T == 0);
+    }
+    t0 = 0;
+    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+    return true;
+  }
+  __device__ __forceinline__ int n() const { return t1 - t0; }
+};
+
+__device__ __forceinline__ void weights_split(const TreeParams& p, WeightBars* bars) {
+  const int lane = threadIdx.x & 31;
+  auto cost = [&](int b) -> int64_t {
+    if (b >= p.B) return 0;
+    int row0, T, ctx;
+    if (!tree_seq(p, b, row0, T, ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, 901);
+    return T ? static_cast<int64_t>((ctx + T + 127) >> 7) * p.Hkv : 0;
+  };
+  int64_t total = 0;
+  for (int b = lane; b < p.B; b += 32) total += cost(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int64_t first = blockIdx.x * total / gridDim.x;
+  const int64_t count = (blockIdx.x + 1) * total / gridDim.x - first;
+  if (lane == 0) {
+    bars->first = first;
+    bars->count = count;
+  }
+  if (count == 0) return;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int64_t w = cost(b0 + lane), incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const bool here = first >= before + incl - w && first < before + incl;
+    if (here) {
+      int row0, T, ctx;
+      tree_seq(p, b0 + lane, row0, T, ctx);
+      const int tiles = (ctx + T + 127) >> 7;
+      const int64_t rest = first - (before + incl - w);
+      bars->b = b0 + lane;
+      bars->g = static_cast<int>(rest / tiles);
+      bars->tile = static_cast<int>(rest % tiles);
+    }
+    if (__any_sync(0xffffffffu, here)) return;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+template <bool KV8>
+__global__ void __launch_bounds__(tr_threads(KV8), 1)
+    cache_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const WeightParams wp) {
+  using SM = WeightSmem<KV8>;
+  constexpr int ITEMS = SM::ITEMS;
+  const TreeParams& p = wp.t;
+  extern __shared__ __align__(1024) uint8_t weights_smem[];
+  uint8_t* smem = weights_smem;
+  WeightBars* bars = reinterpret_cast<WeightBars*>(smem + SM::BAR);
+  const uint32_t q_base = smem_u32(smem);
+  const uint32_t item_base = smem_u32(smem + SM::ITEM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort;
+  if (q_base & 1023u) {
+    if (threadIdx.x == 0) report(HS2_ERR_CUDA, 900);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ITEMS; ++s) {
+      mbar_init(&bars->full[s], KV8 ? 128u : 1u);
+      mbar_init(&bars->empty[s], 1);
+    }
+    if (KV8) {
+      for (int s = 0; s < CW_RAW; ++s) {
+        mbar_init(&bars->raw_full[s], 1);
+        mbar_init(&bars->raw_empty[s], 128);
+      }
+    }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->s_empty[x], 4);
+      mbar_init(&bars->rows_ready[x], 4);
+    }
+    mbar_init(&bars->fin, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_slot, 256);
+    tmem_relinquish();
+  }
+  if (warp == 2) weights_split(p, bars);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_slot;
+
+  if (warp == 0) {
+    // ======================================================== K tiles by TMA
+    WeightWalk w;
+    const bool work = !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars);
+    constexpr int RING = KV8 ? CW_RAW : CW_ITEMS;
+    constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
+    uint64_t* full = KV8 ? bars->raw_full : bars->full;
+    uint64_t* empty = KV8 ? bars->raw_empty : bars->empty;
+    uint8_t* ring = smem + (KV8 ? SM::RAW : SM::ITEM);
+    const int page = 1 << p.page_log2, per_tile = 128 >> p.page_log2;
+    int item = 0;
+    bool ok = work;
+    while (ok) {
+      const int len = w.ctx + w.T;
+      const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+      auto page_of = [&](int t) {
+        const int at = t * 128 + lane * page;
+        return (t < w.t1 && lane < per_tile && at < len) ? table[at >> p.page_log2] : 0;
+      };
+      int pg = page_of(w.t0);
+      for (int t = w.t0; t < w.t1; ++t, ++item) {
+        const int next_pg = page_of(t + 1);
+        const int slot = item % RING;
+        if (item >= RING && !warp_wait(&empty[slot], ((item / RING) - 1) & 1, p.limit_ns, abort_flag, 911)) {
+          ok = false;
+          break;
+        }
+        const int keys = min(128, len - t * 128);
+        const int pages = (keys + page - 1) >> p.page_log2;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(pages << p.page_log2) * (KV8 ? 128u : 256u));
+        __syncwarp();
+        if (lane < pages) {
+          if (pg < 0 || pg >= p.n_pages) {
+            report(HS2_ERR_INDEX, 912);
+            pg = p.n_pages;
+          }
+          uint8_t* dst = ring + slot * SLOT + lane * page * 128;
+          tma_load_3d(dst, &tmK, &full[slot], 0, w.g, pg << p.page_log2);
+          if (!KV8) tma_load_3d(dst + HALF_BYTES, &tmK, &full[slot], 64, w.g, pg << p.page_log2);
+        }
+        pg = next_pg;
+      }
+      if (!ok || !w.next(p)) break;
+    }
+    __syncwarp();
+    if (lane == 0 && work)
+      for (int u = max(0, item - RING); u < item; ++u)
+        wait_done(&full[u % RING], (u / RING) & 1, p.limit_ns, 913);
+  } else if (warp == 1) {
+    // ========================================================== MMA issue
+    WeightWalk w;
+    if (lane == 0 && w.begin(p, bars)) {
+      int item = 0, seg = 0, used[2] = {0, 0};
+      bool ok = true;
+      while (ok) {
+        if (!(ok = mbar_wait(&bars->q_full, seg & 1, p.limit_ns, abort_flag, 921))) break;
+        const int rows = min(p.R, w.T - w.m * p.R) * p.G;
+        const uint32_t cols = static_cast<uint32_t>((rows + 15) & ~15);
+        const uint32_t idesc = idesc_bf16_f32(128, static_cast<int>(cols), 0, 0);
+        const int n = w.n();
+        for (int j = 0; j < n; ++j, ++item) {
+          const int x = j & 1, slot = item % ITEMS;
+          ok = mbar_wait(&bars->full[slot], (item / ITEMS) & 1, p.limit_ns, abort_flag, 922) &&
+               (used[x] == 0 || mbar_wait(&bars->s_empty[x], (used[x] - 1) & 1, p.limit_ns, abort_flag, 923));
+          if (!ok) break;
+          ++used[x];
+          tc_fence_after();
+          const uint32_t kb = item_base + slot * TILE_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
+            umma_ss(tmem + x * 128, sdesc_sw128(kb + koff, 16, 1024), sdesc_sw128(q_base + koff, 16, 1024), idesc,
+                    kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bars->s_full[x]);
+          umma_commit(&bars->empty[slot]);
+        }
+        if (!ok) break;
+        umma_commit(&bars->q_empty);
+        ++seg;
+        if (!w.next(p)) break;
+      }
+      umma_commit(&bars->fin);
+      wait_done(&bars->fin, 0, p.limit_ns, 924);
+    }
+  } else if (warp == 3) {
+    // ======================================================= queries by TMA
+    WeightWalk w;
+    if (lane == 0 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
+      const uint32_t half = static_cast<uint32_t>(p.R * p.G) * 128u;
+      int seg = 0;
+      do {
+        if (seg > 0 && !mbar_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 931)) break;
+        mbar_arrive_expect_tx(&bars->q_full, 2 * half);
+        tma_load_3d(smem, &tmQ, &bars->q_full, 0, w.g * p.G, w.row0 + w.m * p.R);
+        tma_load_3d(smem + HALF_BYTES, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
+        ++seg;
+      } while (w.next(p));
+      wait_done(&bars->q_full, (seg - 1) & 1, p.limit_ns, 932);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ================= sums: thread r of warpgroup x owns key r of its tiles
+    const int x = (warp >= 8) ? 1 : 0;
+    const int r = threadIdx.x - 128 - 128 * x;
+    const uint32_t s_tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 128;
+    int ns = 0, seg = 0;
+    WeightWalk w;
+    bool ok = w.begin(p, bars);
+    while (ok) {
+      const int rows = min(p.R, w.T - w.m * p.R) * p.G;
+      // this segment's query rows: what each sees, and its log-sum.  A buffer is
+      // written again two segments later, after every warp passed the barrier
+      // of the segment between.
+      uint64_t* row_bits = reinterpret_cast<uint64_t*>(smem + SM::BITS) + (x * 2 + (seg & 1)) * 128;
+      float* row_nlse = reinterpret_cast<float*>(smem + SM::NLSE) + (x * 2 + (seg & 1)) * 128;
+      {
+        uint64_t bits = 0;
+        float nl = -INFINITY;
+        const int t = w.m * p.R + r / p.G;
+        if (r < rows) {
+          const int64_t row = w.row0 + t;
+          bits = p.mask ? p.mask[row] : (2ull << t) - 1;
+          if (w.T < 64) bits &= (1ull << w.T) - 1;
+          const float l = wp.lse[static_cast<int64_t>(w.g * p.G + r % p.G) * p.n_tok + row];
+          if ((!wp.counted || wp.counted[row]) && l != -INFINITY) nl = -l * 1.44269504088896340736f;
+        }
+        row_bits[r] = bits;
+        row_nlse[r] = nl;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->rows_ready[x]);
+      if (!warp_wait(&bars->rows_ready[x], seg & 1, p.limit_ns, abort_flag, 942)) break;
+      ++seg;
+      const int len = w.ctx + w.T, n = w.n();
+      const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+      float* acc = wp.acc + (static_cast<int64_t>(w.b) * p.Hkv + w.g) * wp.acc_stride;
+      for (int j = x; j < n; j += 2, ++ns) {
+        const int at = (w.t0 + j) * 128 + r;
+        float old = 0.f, f = p.scale_log2;
+        if (at < len) {
+          old = acc[at];
+          if (KV8) {
+            const int pg = table[at >> p.page_log2];
+            f = 0.f;
+            if (pg >= 0 && pg < p.n_pages)
+              f = p.scale_log2 * p.ksc[((static_cast<int64_t>(pg) << p.page_log2) + (at & ((1 << p.page_log2) - 1))) *
+                                           p.Hkv + w.g];
+          }
+        }
+        if (!(ok = warp_wait(&bars->s_full[x], ns & 1, p.limit_ns, abort_flag, 941))) break;
+        tc_fence_after();
+        const int d = at - w.ctx;  // >= 0: a drafted key
+        const bool drafted = __any_sync(0xffffffffu, d >= 0);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 32) {
+          uint32_t sr[32];
+          tmem_ld32(s_tm + c, sr);
+          tmem_ld_wait();
+          reg_fence(sr);
+          if (!drafted) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float nl = row_nlse[c + e];
+              // a row that collects nothing may hold anything (it may lie behind the batch)
+              const float y = ex2_approx(fmaf(__uint_as_float(sr[e]), f, nl));
+              sum[e & 3] += nl == -INFINITY ? 0.f : y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float nl = row_nlse[c + e];
+              const bool seen = nl != -INFINITY && (d < 0 || (d < 64 && (row_bits[c + e] >> d & 1u)));
+              const float y = ex2_approx(fmaf(__uint_as_float(sr[e]), f, nl));
+              sum[e & 3] += seen ? y : 0.f;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->s_empty[x]);
+        if (at < len) acc[at] = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      }
+      if (!ok || !w.next(p)) break;
+    }
+  } else if (warp >= 12) {
+    // ================================================== e4m3: codes to bf16
+    WeightWalk w;
+    if (KV8 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
+      const int pt = threadIdx.x - 384;
+      const uint32_t raw_base = smem_u32(smem + SM::RAW);
+      int item = 0;
+      bool ok = true;
+      do {
+        for (int t = w.t0; t < w.t1 && ok; ++t, ++item) {
+          const int rs = item % CW_RAW, cs = item % ITEMS;
+          ok = mbar_wait(&bars->raw_full[rs], (item / CW_RAW) & 1, p.limit_ns, abort_flag, 951) &&
+               (item < ITEMS || mbar_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 952));
+          if (!ok) break;
+          convert_tile(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, w.ctx + w.T - t * 128, pt);
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->full[cs]);
+          mbar_arrive(&bars->raw_empty[rs]);
+        }
+      } while (ok && w.next(p));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+}  // namespace hs2

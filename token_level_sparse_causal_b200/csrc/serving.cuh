@@ -3,8 +3,11 @@
 // helpers (tensor maps, shared-memory limits, launch accounting) it uses.
 #pragma once
 
+#include "cache_weights.cuh"
 #include "evict.cuh"
 #include "norm_rope.cuh"
+#include "tree_attn.cuh"
+#include "varlen.cuh"
 
 namespace hs2 {
 namespace {
@@ -49,6 +52,86 @@ int check_cache(const hs2_cache* c, bool table) {
     if (reinterpret_cast<uintptr_t>(c->page_table) & 3u) return HS2_ERR_UNSUPPORTED;
   }
   return HS2_OK;
+}
+
+// 3-D map over e4m3 codes [tokens][heads][128], a box of one head's codes of
+// box_t tokens, not swizzled.
+int make_map_codes(CUtensorMap* m, const void* base, int64_t L, int H, int64_t tok_stride, int64_t head_stride,
+                   int box_t) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || (g_flags & FLAG_FAIL_TMAP)) return HS2_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(HD), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(L)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride), static_cast<cuuint64_t>(tok_stride)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(HD), 1u, static_cast<cuuint32_t>(box_t)};
+  const cuuint32_t es[3] = {1u, 1u, 1u};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? HS2_OK : HS2_ERR_CUDA;
+}
+
+// A map over a pool of the cache, one box per page.
+int make_pool_map(CUtensorMap* m, const hs2_cache* c, const void* pool) {
+  const int tokens = c->n_pages * c->page;
+  return c->kv_dtype == HS2_KV_E4M3
+             ? make_map_codes(m, pool, tokens, c->Hkv, c->tok_stride, c->head_stride, c->page)
+             : make_map(m, pool, tokens, c->Hkv, c->tok_stride, c->head_stride, 1, c->page);
+}
+
+int check_group(int Hq, int Hkv) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv) return HS2_ERR_INVALID_ARG;
+  return Hq / Hkv > kMaxGroup ? HS2_ERR_UNSUPPORTED : HS2_OK;
+}
+
+int check_draft(const hs2_cache* c, const hs2_draft* d) {
+  if (!d || d->n_tok < 0 || d->reserved != 0 || !d->cu_draft || !d->ctx_len) return HS2_ERR_INVALID_ARG;
+  if (d->max_draft < 1 || d->max_draft > 64) return HS2_ERR_INVALID_ARG;
+  if (int rc = check_group(d->Hq, c->Hkv)) return rc;
+  if (int rc = check_rows(d->q_tok_stride, d->q_head_stride, d->Hq, 8)) return rc;
+  if (((reinterpret_cast<uintptr_t>(d->cu_draft) | reinterpret_cast<uintptr_t>(d->ctx_len)) & 3u) ||
+      (reinterpret_cast<uintptr_t>(d->mask) & 7u))
+    return HS2_ERR_UNSUPPORTED;
+  return HS2_OK;
+}
+
+TreeParams tree_params(const hs2_cache* c, const hs2_draft* d) {
+  TreeParams p{};
+  p.B = c->n_seqs;
+  p.Hq = d->Hq;
+  p.Hkv = c->Hkv;
+  p.G = d->Hq / c->Hkv;
+  p.R = 128 / p.G;
+  p.page_log2 = log2_of(c->page);
+  p.n_pages = c->n_pages;
+  p.max_pages = c->max_pages;
+  p.n_tok = d->n_tok;
+  p.max_draft = d->max_draft;
+  p.table = c->page_table;
+  p.cu = d->cu_draft;
+  p.ctx = d->ctx_len;
+  p.mask = d->mask;
+  p.scale_log2 = scale_log2(HD);
+  p.ksc = c->k_scale;
+  p.vsc = c->v_scale;
+  p.limit_ns = g_wait_limit_ns;
+  p.flags = g_flags;
+  return p;
+}
+
+// Workspace of the tree attention: per CTA two parts of up to 128 rows
+// (un-normalised O, then (m, l)) and the unit its last part begins.
+struct TreePlan {
+  int ctas;
+  size_t ml_off, unit_off, bytes;
+};
+
+TreePlan tree_plan() {
+  TreePlan t{};
+  t.ctas = sm_count();
+  t.ml_off = static_cast<size_t>(t.ctas) * 2 * 128 * 128 * sizeof(float);
+  t.unit_off = t.ml_off + static_cast<size_t>(t.ctas) * 2 * 128 * sizeof(float2);
+  t.bytes = t.unit_off + static_cast<size_t>(t.ctas) * sizeof(int4);
+  return t;
 }
 
 template <bool KV8, bool PAIRS>
@@ -175,6 +258,138 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   } else {
     if (int rc = set_smem(cache_evict_kernel<false>, smem)) return rc;
     cache_evict_kernel<false><<<grid, EV_THREADS, smem, st>>>(p);
+  }
+  return launched();
+}
+
+int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const void* v, const int32_t* cu_q,
+                    const int32_t* cu_k, void* o, float* lse, void* stream) {
+  using namespace hs2;
+  const hs2_varlen* s = shape;
+  if (!s || s->n_seqs <= 0 || s->total_q < 0 || s->total_k < 0) return HS2_ERR_INVALID_ARG;
+  if (int rc = check_group(s->Hq, s->Hkv)) return rc;
+  if (s->d != HD || s->n_seqs > kMaxSeqs) return HS2_ERR_UNSUPPORTED;
+  if (int rc = check_rows(s->q_tok_stride, s->q_head_stride, s->Hq, 8)) return rc;
+  if (int rc = check_rows(s->kv_tok_stride, s->kv_head_stride, s->Hkv, 8)) return rc;
+  if (!cu_q) return HS2_ERR_INVALID_ARG;
+  if (s->total_q == 0) return HS2_OK;
+  if (!q || !o || (s->total_k > 0 && (!k || !v))) return HS2_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3u))
+    return HS2_ERR_UNSUPPORTED;
+  VarlenParams p{};
+  p.B = s->n_seqs;
+  p.total_q = s->total_q;
+  p.total_k = s->total_k;
+  p.Hq = s->Hq;
+  p.Hkv = s->Hkv;
+  p.G = s->Hq / s->Hkv;
+  p.rows_tok = 128 / p.G;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k ? cu_k : cu_q;
+  p.scale_log2 = scale_log2(HD);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_tok = s->q_tok_stride;
+  p.o_head = s->q_head_stride;
+  p.lse = lse;
+  p.limit_ns = g_wait_limit_ns;
+  p.flags = g_flags;
+  // at least one item per KV head for every pair of tiles any split of
+  // total_q tokens into n_seqs sequences can have
+  const int64_t items = s->total_q / (2 * p.rows_tok) + s->n_seqs;
+  if (items * s->Hkv > (int64_t(1) << 31) - 1) return HS2_ERR_UNSUPPORTED;
+  CUtensorMap mq, mk, mv;
+  if (int rc = make_map(&mq, q, s->total_q, s->Hq, s->q_tok_stride, s->q_head_stride, p.G, p.rows_tok)) return rc;
+  mk = mv = mq;  // without keys no tile of them is loaded
+  if (s->total_k > 0) {
+    if (int rc = make_map(&mk, k, s->total_k, s->Hkv, s->kv_tok_stride, s->kv_head_stride, 1, 128)) return rc;
+    if (int rc = make_map(&mv, v, s->total_k, s->Hkv, s->kv_tok_stride, s->kv_head_stride, 1, 128)) return rc;
+  }
+  if (int rc = set_smem(varlen_attn_kernel, FL_SMEM_DENSE)) return rc;
+  const Range range("hs2 varlen_attn");
+  varlen_attn_kernel<<<static_cast<unsigned>(items * s->Hkv), FL_THREADS, FL_SMEM_DENSE,
+                       static_cast<cudaStream_t>(stream)>>>(mq, mk, mv, p);
+  return launched();
+}
+
+int hs2_tree_attn_workspace(const hs2_cache* cache, const hs2_draft* draft, size_t* workspace_bytes) {
+  using namespace hs2;
+  if (int rc = check_cache(cache, true)) return rc;
+  if (int rc = check_draft(cache, draft)) return rc;
+  if (!workspace_bytes) return HS2_ERR_INVALID_ARG;
+  *workspace_bytes = tree_plan().bytes;
+  return HS2_OK;
+}
+
+int hs2_tree_attn(const hs2_cache* cache, const hs2_draft* draft, const void* q, void* o, float* lse,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace hs2;
+  if (int rc = check_cache(cache, true)) return rc;
+  if (int rc = check_draft(cache, draft)) return rc;
+  if (draft->n_tok == 0) return HS2_OK;
+  if (!q || !o || !workspace) return HS2_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return HS2_ERR_UNSUPPORTED;
+  const TreePlan plan = tree_plan();
+  if (workspace_bytes < plan.bytes) return HS2_ERR_WORKSPACE;
+  TreeParams p = tree_params(cache, draft);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.o_tok = draft->q_tok_stride;
+  p.o_head = draft->q_head_stride;
+  p.lse = lse;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(w);
+  p.part_ml = reinterpret_cast<float2*>(w + plan.ml_off);
+  p.part_unit = reinterpret_cast<int4*>(w + plan.unit_off);
+  CUtensorMap mq, mk, mv;
+  if (int rc = make_map(&mq, q, draft->n_tok, draft->Hq, draft->q_tok_stride, draft->q_head_stride, p.G, p.R))
+    return rc;
+  if (int rc = make_pool_map(&mk, cache, cache->k)) return rc;
+  if (int rc = make_pool_map(&mv, cache, cache->v)) return rc;
+  const Range range("hs2 tree_attn");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(plan.ctas);
+  if (cache->kv_dtype == HS2_KV_E4M3) {
+    if (int rc = set_smem(tree_attn_kernel<true>, TreeSmem<true>::BYTES)) return rc;
+    tree_attn_kernel<true><<<grid, tr_threads(true), TreeSmem<true>::BYTES, st>>>(mq, mk, mv, p);
+  } else {
+    if (int rc = set_smem(tree_attn_kernel<false>, TreeSmem<false>::BYTES)) return rc;
+    tree_attn_kernel<false><<<grid, tr_threads(false), TreeSmem<false>::BYTES, st>>>(mq, mk, mv, p);
+  }
+  if (int rc = launched()) return rc;
+  const int rows = std::min(p.R, draft->max_draft) * p.G;  // of a unit
+  tree_merge_kernel<<<dim3(grid, static_cast<unsigned>((rows + 3) / 4)), 128, 0, st>>>(p);
+  return launched();
+}
+
+int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void* q, const float* lse,
+                      const uint8_t* counted, float* acc, int64_t acc_stride, void* stream) {
+  using namespace hs2;
+  if (int rc = check_cache(cache, true)) return rc;
+  if (int rc = check_draft(cache, draft)) return rc;
+  if (acc_stride <= 0 || acc_stride % 4) return HS2_ERR_INVALID_ARG;
+  if (draft->n_tok == 0) return HS2_OK;
+  if (!q || !lse || !acc) return HS2_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(acc) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return HS2_ERR_UNSUPPORTED;
+  WeightParams p{};
+  p.t = tree_params(cache, draft);
+  p.lse = lse;
+  p.counted = counted;
+  p.acc = acc;
+  p.acc_stride = acc_stride;
+  CUtensorMap mq, mk;
+  if (int rc = make_map(&mq, q, draft->n_tok, draft->Hq, draft->q_tok_stride, draft->q_head_stride, p.t.G, p.t.R))
+    return rc;
+  if (int rc = make_pool_map(&mk, cache, cache->k)) return rc;
+  const Range range("hs2 cache_weights");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(sm_count());
+  if (cache->kv_dtype == HS2_KV_E4M3) {
+    if (int rc = set_smem(cache_weights_kernel<true>, WeightSmem<true>::BYTES)) return rc;
+    cache_weights_kernel<true><<<grid, tr_threads(true), WeightSmem<true>::BYTES, st>>>(mq, mk, p);
+  } else {
+    if (int rc = set_smem(cache_weights_kernel<false>, WeightSmem<false>::BYTES)) return rc;
+    cache_weights_kernel<false><<<grid, tr_threads(false), WeightSmem<false>::BYTES, st>>>(mq, mk, p);
   }
   return launched();
 }

@@ -1,0 +1,772 @@
+// Attention of drafted tokens over a paged cache: each of a sequence's T
+// drafted tokens (T * G query rows per KV head) sees all committed tokens and
+// the drafted ones its mask names; T = 1 is ordinary decoding.
+//
+// Bound by memory: K and V are read once (512 B per key and KV head in bf16,
+// 264 B as e4m3 with scales), and at T * G <= 128 rows one pass over them
+// serves all rows.  So the design is about keeping loads in flight:
+//
+//   work     the unit is (sequence, KV head, tile of 128 / G tokens); all units'
+//            key tiles (128 keys) are laid end to end and every CTA (one per
+//            SM, persistent) takes an equal stretch, whatever the lengths: one
+//            long context is spread over all SMs, many short ones are packed.
+//            A stretch that holds only part of a unit leaves (m, l, O) in the
+//            workspace and tree_merge_kernel joins the parts in key order, so
+//            results do not depend on timing;
+//   ring     one ring of tiles in the order the products use them, K0 K1 V0 K2
+//            V1 K3 ..., filled by TMA through the page table (a box per page)
+//            without regard to unit borders: loads of the next unit run while
+//            the last one finishes;
+//   overlap  even and odd key tiles of a unit are two independent softmaxes
+//            (own S, P, O in tensor memory, own warpgroup) that take turns on
+//            the tensor core as in flash.cuh; their O join in the epilogue,
+//            where each warpgroup writes half of the columns;
+//   e4m3     codes arrive by TMA in a raw ring; four warps turn them into bf16
+//            (exact; unlike f16 it leaves Q and P their whole range), another
+//            fetches the scales; the K scale multiplies the scores, the V
+//            scale multiplies P before its rounding;
+//   edges    columns without a visible key become -inf whatever they hold, V
+//            rows behind the last key are zeroed before the product.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attn_tile.cuh"
+
+namespace hs2 {
+
+constexpr int TR_ITEMS = 6;      // bf16: tiles of 32 KB in the ring
+constexpr int TR_ITEMS_KV8 = 3;  // e4m3: converted tiles
+constexpr int TR_RAW = 5;        // e4m3: raw tiles of 16 KB
+constexpr int TR_SCALES = 4;     // e4m3: key tiles whose scales are held
+constexpr uint32_t RAW_BYTES = 128u * 128u;
+__host__ __device__ constexpr int tr_threads(bool kv8) { return kv8 ? 512 : 384; }
+
+// What a call's kernels share: the unit geometry.
+struct TreeParams {
+  int B, Hq, Hkv, G, R, page_log2, n_pages, max_pages, n_tok, max_draft;
+  const int32_t *table, *cu, *ctx;
+  const uint64_t* mask;
+  float scale_log2;
+  const float *ksc, *vsc;  // e4m3 only
+  __nv_bfloat16* o;
+  int64_t o_tok, o_head;
+  float* lse;
+  float* part_o;    // [CTA][2][128][128], un-normalised
+  float2* part_ml;  // [CTA][2][128]
+  int4* part_unit;  // [CTA]: (sequence, KV head, tile, last CTA) of the unit whose first part this CTA holds
+  uint64_t limit_ns;
+  uint32_t flags;
+};
+
+struct TreeBars {
+  uint64_t full[TR_ITEMS], empty[TR_ITEMS];
+  uint64_t raw_full[TR_RAW], raw_empty[TR_RAW];
+  uint64_t sc_full[TR_SCALES], sc_empty[TR_SCALES];
+  uint64_t q_full, q_empty;
+  uint64_t v_raw[TR_ITEMS];  // a V tile landed whose rows behind the sequence are not yet zeroed
+  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t ml_ready, o_free;
+  uint64_t fin;
+  int64_t first;  // this CTA's stretch: first tile, number of tiles
+  int64_t count;
+  int64_t total;
+  int b, unit, tile;  // where the stretch begins
+  int parts;          // CTAs that have work
+  uint32_t tmem_slot;
+  int abort;
+};
+static_assert(sizeof(TreeBars) <= 512, "barrier area");
+
+template <bool KV8>
+struct TreeSmem {
+  static constexpr int ITEMS = KV8 ? TR_ITEMS_KV8 : TR_ITEMS;
+  static constexpr uint32_t ITEM = TILE_BYTES;  // after Q
+  static constexpr uint32_t RAW = ITEM + ITEMS * TILE_BYTES;
+  static constexpr uint32_t SCALE = RAW + (KV8 ? TR_RAW * RAW_BYTES : 0u);
+  static constexpr uint32_t BAR = SCALE + (KV8 ? TR_SCALES * 1024u : 0u);
+  static constexpr uint32_t ML = BAR + 512u;  // float2 [2][128]
+  static constexpr uint32_t BYTES = ML + 2048u;
+  static_assert(BYTES <= 232448u, "shared memory of one CTA");
+};
+
+// A sequence's lengths; a bad entry counts as no drafted tokens.
+__device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, int& row0, int& T, int& ctx) {
+  const int64_t r0 = p.cu[b], t = static_cast<int64_t>(p.cu[b + 1]) - r0, c = p.ctx[b];
+  const bool ok = r0 >= 0 && t >= 0 && t <= p.max_draft && r0 + t <= p.n_tok && c >= 0 &&
+                  c + t <= (static_cast<int64_t>(p.max_pages) << p.page_log2);
+  row0 = ok ? static_cast<int>(r0) : 0;
+  T = ok ? static_cast<int>(t) : 0;
+  ctx = ok ? static_cast<int>(c) : 0;
+  return ok;
+}
+
+// Walks the segments (parts of units) of one CTA's stretch; every role of the
+// CTA walks the same ones.
+struct TreeWalk {
+  int b, g, m;          // unit
+  int row0, T, ctx;     // its sequence
+  int tiles, mtiles;    // key tiles of the unit, token tiles of the sequence
+  int t0, t1;           // the segment's key tiles
+  int64_t left, pos;    // tiles left in the stretch, global index of t0
+
+  __device__ __forceinline__ void load(const TreeParams& p) {
+    tree_seq(p, b, row0, T, ctx);
+    tiles = T ? (ctx + T + 127) >> 7 : 0;
+    mtiles = (T + p.R - 1) / p.R;
+  }
+  __device__ __forceinline__ bool begin(const TreeParams& p, const TreeBars* bars) {
+    left = bars->count;
+    if (left <= 0) return false;
+    pos = bars->first;
+    b = bars->b;
+    load(p);
+    g = bars->unit / mtiles;
+    m = bars->unit % mtiles;
+    t0 = bars->tile;
+    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + left));
+    return true;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    left -= t1 - t0;
+    pos += t1 - t0;
+    if (left <= 0) return false;
+    if (++m == mtiles) {
+      m = 0;
+      if (++g == p.Hkv) {
+        g = 0;
+        do {
+          ++b;
+          load(p);
+        } while (T == 0);  // tiles are left, so a sequence with some follows
+      }
+    }
+    t0 = 0;
+    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+    return true;
+  }
+  __device__ __forceinline__ int n() const { return t1 - t0; }
+  __device__ __forceinline__ int rows(const TreeParams& p) const { return min(p.R, T - m * p.R) * p.G; }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+  // rows of the segment's last tile that are keys (128: all)
+  __device__ __forceinline__ int last_rows() const { return t1 == tiles ? ctx + T - (tiles - 1) * 128 : 128; }
+};
+
+// One warp splits all tiles evenly and finds where this CTA's stretch begins.
+__device__ __forceinline__ void tree_split(const TreeParams& p, TreeBars* bars) {
+  const int lane = threadIdx.x & 31;
+  auto cost = [&](int b) -> int64_t {
+    if (b >= p.B) return 0;
+    int row0, T, ctx;
+    if (!tree_seq(p, b, row0, T, ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, 801);
+    return T ? static_cast<int64_t>((ctx + T + 127) >> 7) * p.Hkv * ((T + p.R - 1) / p.R) : 0;
+  };
+  int64_t total = 0;
+  for (int b = lane; b < p.B; b += 32) total += cost(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  const int c = blockIdx.x;
+  int64_t first = 0, count = 0;
+  if (c < parts) {
+    first = c * total / parts;
+    count = (c + 1) * total / parts - first;
+  }
+  if (lane == 0) {
+    bars->first = first;
+    bars->count = count;
+    bars->total = total;
+    bars->parts = parts;
+  }
+  if (count == 0) return;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int64_t w = cost(b0 + lane), incl = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const bool here = first >= before + incl - w && first < before + incl;
+    if (here) {
+      int row0, T, ctx;
+      tree_seq(p, b0 + lane, row0, T, ctx);
+      const int tiles = (ctx + T + 127) >> 7;
+      const int64_t rest = first - (before + incl - w);
+      bars->b = b0 + lane;
+      bars->unit = static_cast<int>(rest / tiles);
+      bars->tile = static_cast<int>(rest % tiles);
+    }
+    if (__any_sync(0xffffffffu, here)) return;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The tile that is item u of a segment of n tiles (K0 K1 V0 K2 V1 ... ): its
+// index, and whether it is a V tile.
+__device__ __forceinline__ void tree_item(int u, int n, int& tile, bool& is_v) {
+  if (u == 0 || n == 1) {
+    tile = 0;
+    is_v = u == 1;
+  } else if (u == 1) {
+    tile = 1;
+    is_v = false;
+  } else if (u >= 2 * n - 2) {  // the last two V follow each other
+    tile = u - n;
+    is_v = true;
+  } else {
+    is_v = (u & 1) == 0;
+    tile = is_v ? (u - 2) >> 1 : (u + 1) >> 1;
+  }
+}
+
+// Columns of key tile j (first key at `base`) that a row with draft bits
+// `bits` sees, as 4 words.
+__device__ __forceinline__ void tree_visible(int ctx, int base, uint64_t bits, uint32_t (&w)[4]) {
+  const int d = ctx - base;  // columns before the first drafted key
+  uint64_t lo = 0, hi = 0;
+  if (d >= 128) {
+    lo = hi = ~0ull;
+  } else if (d >= 64) {
+    const int s = d - 64;
+    lo = ~0ull;
+    hi = ((1ull << s) - 1) | (bits << s);
+  } else if (d > 0) {
+    lo = ((1ull << d) - 1) | (bits << d);
+    hi = bits >> (64 - d);
+  } else if (d > -64) {
+    lo = bits >> -d;
+  }
+  w[0] = static_cast<uint32_t>(lo);
+  w[1] = static_cast<uint32_t>(lo >> 32);
+  w[2] = static_cast<uint32_t>(hi);
+  w[3] = static_cast<uint32_t>(hi >> 32);
+}
+
+// Sixteen e4m3 codes -> sixteen bf16 values (exact, NaN stays NaN).
+__device__ __forceinline__ void e4m3x16_to_bf16(uint4 raw, uint4& a, uint4& b) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t f[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t h = e4m3x2_to_f16x2(w[q >> 1] >> (16 * (q & 1)));
+    const __half2 h2 = *reinterpret_cast<const __half2*>(&h);
+    const float2 v = __half22float2(h2);
+    f[q] = pack_bf16x2(v.x, v.y);
+  }
+  a = make_uint4(f[0], f[1], f[2], f[3]);
+  b = make_uint4(f[4], f[5], f[6], f[7]);
+}
+
+// A raw tile of 128 rows of codes -> a bf16 tile in two 128-byte-swizzled
+// halves, by 128 threads (pt); rows from `keys` on become zeros.
+__device__ __forceinline__ void convert_tile(uint32_t raw_tile, uint32_t tile, int keys, int pt) {
+  const int c8 = pt & 7, row0 = pt >> 3;
+  uint4 raw[8];
+#pragma unroll
+  for (int it = 0; it < 8; ++it) raw[it] = ld_shared_v4(raw_tile + (row0 + 16 * it) * 128 + c8 * 16);
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int row = row0 + 16 * it;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (row < keys) e4m3x16_to_bf16(raw[it], a, b);
+    // lanes 0-3 and 4-7 of a row store their two chunks in opposite order, so
+    // that a store touches every bank once
+    const bool flip = c8 >= 4;
+    st_shared_v4(tile + sw128_chunk_offset(row, 2 * c8 + (flip ? 1 : 0), 128), flip ? b : a);
+    st_shared_v4(tile + sw128_chunk_offset(row, 2 * c8 + (flip ? 0 : 1), 128), flip ? a : b);
+  }
+}
+
+template <bool KV8>
+__global__ void __launch_bounds__(tr_threads(KV8), 1)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const TreeParams p) {
+  using SM = TreeSmem<KV8>;
+  constexpr int ITEMS = SM::ITEMS;
+  extern __shared__ __align__(1024) uint8_t tree_smem[];
+  uint8_t* smem = tree_smem;
+  TreeBars* bars = reinterpret_cast<TreeBars*>(smem + SM::BAR);
+  float2* ml = reinterpret_cast<float2*>(smem + SM::ML);
+  float* scales = reinterpret_cast<float*>(smem + SM::SCALE);  // [slot][K, V][128]
+  const uint32_t q_base = smem_u32(smem);
+  const uint32_t item_base = smem_u32(smem + SM::ITEM);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars->abort;
+  if (q_base & 1023u) {  // the swizzled tiles need it; the whole CTA leaves
+    if (threadIdx.x == 0) {
+      p.part_unit[blockIdx.x] = make_int4(0, 0, 0, -1);
+      report(HS2_ERR_CUDA, 800);
+    }
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ITEMS; ++s) {
+      mbar_init(&bars->full[s], KV8 ? 128u : 1u);
+      mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->v_raw[s], 1);
+    }
+    if (KV8) {
+      for (int s = 0; s < TR_RAW; ++s) {
+        mbar_init(&bars->raw_full[s], 1);
+        mbar_init(&bars->raw_empty[s], 128);
+      }
+      for (int s = 0; s < TR_SCALES; ++s) {
+        mbar_init(&bars->sc_full[s], 32);
+        mbar_init(&bars->sc_empty[s], 4);
+      }
+    }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->p_ready[x], 4);
+      mbar_init(&bars->o_done[x], 1);
+    }
+    mbar_init(&bars->ml_ready, 8);
+    mbar_init(&bars->o_free, 8);
+    mbar_init(&bars->fin, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 2) tree_split(p, bars);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_slot;
+  // Registers move to the two softmax warpgroups (a row of scores is 128 of
+  // them); the shares of all warpgroups add up to what the CTA was launched
+  // with: 3 x 168 = 2 x 208 + 88, with an e4m3 cache 4 x 128 = 2 x 184 + 2 x 72.
+  if (warp >= 4 && warp < 12) {
+    reg_acquire<KV8 ? 184 : 208>();
+    // ============================================ softmax / rescale / epilogue
+    const int x = (warp >= 8) ? 1 : 0;
+    const int r = threadIdx.x - 128 - 128 * x;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_off + x * 128;
+    const uint32_t o_tm = tmem + lane_off + 256;  // O of x at + 128 x
+    const int tok_r = r / p.G, head_r = r % p.G;
+    int ns = 0, no1 = 0, seg = 0, ti = 0;  // waits taken on s_full[x] and o_done[1]; segments; tiles
+    TreeWalk w;
+    bool ok = w.begin(p, bars);
+    if (threadIdx.x == 128) p.part_unit[blockIdx.x] = make_int4(0, 0, 0, -1);  // also if a wait runs out below
+    while (ok) {
+      const int n = w.n();
+      const int t = w.m * p.R + tok_r;
+      const bool row_live = r < p.R * p.G && t < w.T;
+      const bool warp_live = (warp & 3) * 32 < w.rows(p);
+      uint64_t bits = 0;
+      if (row_live) {
+        bits = p.mask ? p.mask[w.row0 + t] : (2ull << t) - 1;  // t = 63: 2 << 63 = 0, minus 1: all
+        if (w.T < 64) bits &= (1ull << w.T) - 1;
+      }
+      RowState st;
+      for (int j = x; j < n; j += 2, ++ns) {
+        if (!(ok = warp_wait(&bars->s_full[x], ns & 1, p.limit_ns, abort_flag, 841))) break;
+        tc_fence_after();
+        const float* sc_s = nullptr;
+        if (KV8) {
+          const int slot = (ti + j) % TR_SCALES;
+          if (!(ok = warp_wait(&bars->sc_full[slot], ((ti + j) / TR_SCALES) & 1, p.limit_ns, abort_flag, 842))) break;
+          sc_s = scales + slot * 256;
+        }
+        if (warp_live) {
+          uint32_t sr[4][32];
+          load_scores(s_tm, sr);
+          if (KV8) {
+            const uint64_t* ks2 = reinterpret_cast<const uint64_t*>(sc_s);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              float a0, a1;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(sr[c >> 4][2 * (c & 15)]),
+                                       __uint_as_float(sr[c >> 4][2 * (c & 15) + 1])),
+                               ks2[c]),
+                        a0, a1);
+              sr[c >> 4][2 * (c & 15)] = __float_as_uint(a0);
+              sr[c >> 4][2 * (c & 15) + 1] = __float_as_uint(a1);
+            }
+          }
+          const int base = (w.t0 + j) * 128;
+          if (base + 128 > w.ctx) {
+            uint32_t vis[4];
+            tree_visible(w.ctx, base, bits, vis);
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (!(vis[c >> 5] >> (c & 31) & 1u)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          }
+          float alpha;
+          const bool resc =
+              softmax_tile<KV8>(s_tm, sr, KV8 ? 1.f : p.scale_log2, KV8 ? sc_s + 128 : nullptr, st, alpha);
+          // P V(j - 2) completed before S(j): s_full's commit covers it
+          if (j >= 2 && __any_sync(0xffffffffu, resc)) rescale_row(o_tm + 128 * x, alpha);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->p_ready[x]);
+          if (KV8) mbar_arrive(&bars->sc_empty[(ti + j) % TR_SCALES]);
+        }
+      }
+      if (!ok) break;
+      // ---- epilogue: join the even and the odd tiles' O.  Once O is done the
+      // (m, l) area is free: this segment's products waited (o_free) for every
+      // warp to be through with the last segment's.
+      ok = warp_wait(&bars->o_done[0], seg & 1, p.limit_ns, abort_flag, 843);
+      if (ok && n > 1) ok = warp_wait(&bars->o_done[1], no1++ & 1, p.limit_ns, abort_flag, 845);
+      if (!ok) break;
+      ml[x * 128 + r] = make_float2(st.m, st.l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->ml_ready);
+      if (!(ok = warp_wait(&bars->ml_ready, seg & 1, p.limit_ns, abort_flag, 844))) break;
+      tc_fence_after();
+      if (warp_live) {
+        const float2 a = ml[r], c2 = ml[128 + r];
+        const float M = fmaxf(a.x, c2.x);
+        const float wa = (a.x == -INFINITY) ? 0.f : ex2_approx(a.x - M);
+        const float wb = (c2.x == -INFINITY) ? 0.f : ex2_approx(c2.x - M);
+        const float L = a.y * wa + c2.y * wb;
+        const bool whole = w.whole();
+        const float inv = !whole ? 1.f : (L > 0.f ? 1.f / L : 0.f);
+        const int64_t row = w.row0 + t;
+        const int h = w.g * p.G + head_r;
+        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 == 0 ? 1 : 0);
+#pragma unroll 1
+        for (int c = 2 * x; c < 2 * x + 2; ++c) {  // this warpgroup's half of the columns
+          uint32_t oa[32], ob[32];
+          tmem_ld32(o_tm + c * 32, oa);
+          if (n > 1) tmem_ld32(o_tm + 128 + c * 32, ob);
+          tmem_ld_wait();
+          reg_fence(oa);
+          if (n > 1) reg_fence(ob);
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            // an O without a visible key holds nothing to add, whatever is there
+            float y = wa > 0.f ? __uint_as_float(oa[e]) * wa : 0.f;
+            if (n > 1 && wb > 0.f) y = fmaf(__uint_as_float(ob[e]), wb, y);
+            v[e] = y * inv;
+          }
+          if (row_live && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                  pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+          } else if (row_live) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * 128 + r) * 128 + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+        }
+        if (row_live && x == 0) {
+          if (!whole)
+            p.part_ml[slot * 128 + r] = make_float2(M, L);
+          else if (p.lse)
+            p.lse[static_cast<int64_t>(h) * p.n_tok + row] = (M + log2f(L)) * 0.69314718055994530942f;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->o_free);
+      ti += n;
+      ++seg;
+      // the stretch's last segment may be a unit's first part
+      if (threadIdx.x == 128 && w.left == n) {
+        const bool head = w.t0 == 0 && w.t1 < w.tiles;
+        const int64_t end = w.pos + w.tiles;  // of the unit (its segment begins at tile 0)
+        p.part_unit[blockIdx.x] =
+            make_int4(w.b, w.g, w.m, head ? static_cast<int>((end * bars->parts - 1) / bars->total) : -1);
+      }
+      if (!w.next(p)) break;
+    }
+  } else {
+    reg_release<KV8 ? 72 : 88>();
+    if (warp == 0) {
+      // =========================================================== TMA loads
+      TreeWalk w;
+      const bool work = !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars);
+      constexpr int RING = KV8 ? TR_RAW : TR_ITEMS;
+      constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
+      uint64_t* full = KV8 ? bars->raw_full : bars->full;
+      uint64_t* empty = KV8 ? bars->raw_empty : bars->empty;
+      uint8_t* ring = smem + (KV8 ? SM::RAW : SM::ITEM);
+      const int page = 1 << p.page_log2, per_tile = 128 >> p.page_log2;
+      int item = 0;
+      uint32_t raw_used = 0, raw_uses = 0;  // slots last filled through v_raw, and how often (mod 2)
+      bool ok = work;
+      while (ok) {
+        const int n = w.n(), len = w.ctx + w.T;
+        const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+        // each lane's page of an item, read one item ahead of its use
+        auto page_of = [&](int u) {
+          int tile;
+          bool is_v;
+          tree_item(u, n, tile, is_v);
+          const int at = (w.t0 + tile) * 128 + lane * page;
+          return (u < 2 * n && lane < per_tile && at < len) ? table[at >> p.page_log2] : 0;
+        };
+        int pg = page_of(0);
+        for (int u = 0; u < 2 * n; ++u, ++item) {
+          int tile;
+          bool is_v;
+          tree_item(u, n, tile, is_v);
+          const int next_pg = page_of(u + 1);
+          const int slot = item % RING;
+          if (item >= RING && !warp_wait(&empty[slot], ((item / RING) - 1) & 1, p.limit_ns, abort_flag, 812)) {
+            ok = false;
+            break;
+          }
+          const int keys = min(128, len - (w.t0 + tile) * 128);
+          const int pages = (keys + page - 1) >> p.page_log2;  // the rest of the tile is not loaded
+          // a last V tile to be mended reaches `full` through warp 2
+          const bool mend = !KV8 && is_v && tile == n - 1 && w.last_rows() < 128;
+          uint64_t* bar = mend ? &bars->v_raw[slot] : &full[slot];
+          raw_used = (raw_used & ~(1u << slot)) | (mend ? 1u << slot : 0u);
+          raw_uses ^= mend ? 1u << slot : 0u;
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(pages << p.page_log2) * (KV8 ? 128u : 256u));
+          __syncwarp();
+          if (lane < pages) {
+            if (pg < 0 || pg >= p.n_pages) {
+              report(HS2_ERR_INDEX, 813);
+              pg = p.n_pages;  // behind the pools: reads as zeros
+            }
+            const CUtensorMap* map = is_v ? &tmV : &tmK;
+            uint8_t* dst = ring + slot * SLOT + lane * page * 128;
+            const int tok = pg << p.page_log2;
+            tma_load_3d(dst, map, bar, 0, w.g, tok);
+            if (!KV8) tma_load_3d(dst + HALF_BYTES, map, bar, 64, w.g, tok);
+          }
+          pg = next_pg;
+        }
+        if (!ok || !w.next(p)) break;
+      }
+      // never leave a TMA write in flight into memory the CTA gives back
+      __syncwarp();
+      if (lane == 0 && work)
+        for (int u = max(0, item - RING); u < item; ++u)
+          if (raw_used >> (u % RING) & 1u)
+            wait_done(&bars->v_raw[u % RING], ~(raw_uses >> (u % RING)) & 1u, p.limit_ns, 817);
+          else
+            wait_done(&full[u % RING], (u / RING) & 1, p.limit_ns, 814);
+    } else if (warp == 1) {
+      // ========================================================== MMA issue
+      TreeWalk w;
+      if (lane == 0 && w.begin(p, bars)) {
+        int item = 0, seg = 0, np[2] = {0, 0};
+        bool ok = true;
+        auto wait_item = [&](int u) {
+          return mbar_wait(&bars->full[u % ITEMS], (u / ITEMS) & 1, p.limit_ns, abort_flag, 821);
+        };
+        auto issue_s = [&](int x, int u, bool last) {
+          const uint32_t kb = item_base + (u % ITEMS) * TILE_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
+            umma_ss(tmem + x * 128, sdesc_sw128(q_base + koff, 16, 1024), sdesc_sw128(kb + koff, 16, 1024), IDESC_S,
+                    kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bars->s_full[x]);
+          umma_commit(&bars->empty[u % ITEMS]);
+          if (last) umma_commit(&bars->q_empty);
+        };
+        auto issue_pv = [&](int x, int u, bool first, bool last) {
+          const uint32_t vb = item_base + (u % ITEMS) * TILE_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 2048, HALF_BYTES, 1024),
+                    IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->empty[u % ITEMS]);
+          if (last) umma_commit(&bars->o_done[x]);
+        };
+        while (ok) {
+          const int n = w.n();
+          ok = mbar_wait(&bars->q_full, seg & 1, p.limit_ns, abort_flag, 822) && wait_item(item);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0, item++, n == 1);
+          if (n > 1) {
+            if (!(ok = wait_item(item))) break;
+            tc_fence_after();
+            issue_s(1, item++, n == 2);
+          }
+          for (int j = 0; j < n; ++j) {
+            const int x = j & 1;
+            // V(j) and K(j + 2) normally landed long ago: nothing but P stands
+            // between its arrival and the products
+            ok = wait_item(item) && (j + 2 >= n || wait_item(item + 1));
+            // the last segment's O has been read
+            if (ok && j == 0 && seg > 0) ok = mbar_wait(&bars->o_free, (seg - 1) & 1, p.limit_ns, abort_flag, 824);
+            if (ok) ok = mbar_wait(&bars->p_ready[x], np[x]++ & 1, p.limit_ns, abort_flag, 825);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(x, item++, j < 2, j + 2 >= n);
+            if (j + 2 < n) issue_s(x, item++, j + 3 == n);
+          }
+          ++seg;
+          if (!ok || !w.next(p)) break;
+        }
+        umma_commit(&bars->fin);
+        wait_done(&bars->fin, 0, p.limit_ns, 826);
+      }
+    } else if (warp == 3) {
+      // ======================= a segment's queries, once the last one's products
+      // have read theirs (the K / V loads above do not wait for that)
+      TreeWalk w;
+      if (lane == 0 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
+        const uint32_t half = static_cast<uint32_t>(p.R * p.G) * 128u;
+        int seg = 0;
+        do {
+          if (seg > 0 && !mbar_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 816)) break;
+          mbar_arrive_expect_tx(&bars->q_full, 2 * half);
+          tma_load_3d(smem, &tmQ, &bars->q_full, 0, w.g * p.G, w.row0 + w.m * p.R);
+          tma_load_3d(smem + HALF_BYTES, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
+          ++seg;
+        } while (w.next(p));
+        wait_done(&bars->q_full, (seg - 1) & 1, p.limit_ns, 815);
+      }
+    } else if (warp == 2) {
+      TreeWalk w;
+      if (!(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
+        if (!KV8) {
+          // ================================ V rows behind the sequence's last key
+          int item = 0;
+          uint32_t uses = 0;  // of each slot's v_raw, mod 2
+          do {
+            item += 2 * w.n();
+            if (w.last_rows() < 128) {
+              const int slot = (item - 1) % ITEMS;  // a segment's last item is its last V tile
+              if (!warp_wait(&bars->v_raw[slot], uses >> slot & 1u, p.limit_ns, abort_flag, 831)) break;
+              uses ^= 1u << slot;
+              zero_rows(item_base + slot * TILE_BYTES, w.last_rows(), lane, 32);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->full[slot]);
+            }
+          } while (w.next(p));
+        } else {
+          // ================================================ scales of the keys
+          int ti = 0;
+          bool ok = true;
+          do {
+            const int len = w.ctx + w.T;
+            const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+            for (int t = w.t0; t < w.t1 && ok; ++t, ++ti) {
+              float ks[4], vs[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int at = t * 128 + lane + 32 * e;
+                ks[e] = vs[e] = 0.f;
+                if (at < len) {
+                  const int pg = table[at >> p.page_log2];
+                  if (pg >= 0 && pg < p.n_pages) {
+                    const int64_t tok = (static_cast<int64_t>(pg) << p.page_log2) + (at & ((1 << p.page_log2) - 1));
+                    ks[e] = p.ksc[tok * p.Hkv + w.g] * p.scale_log2;
+                    vs[e] = p.vsc[tok * p.Hkv + w.g];
+                  }
+                }
+              }
+              const int slot = ti % TR_SCALES;
+              if (ti >= TR_SCALES &&
+                  !mbar_wait(&bars->sc_empty[slot], ((ti / TR_SCALES) - 1) & 1, p.limit_ns, abort_flag, 832)) {
+                ok = false;
+                break;
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                scales[slot * 256 + lane + 32 * e] = ks[e];
+                scales[slot * 256 + 128 + lane + 32 * e] = vs[e];
+              }
+              mbar_arrive(&bars->sc_full[slot]);
+            }
+          } while (ok && w.next(p));
+        }
+      }
+    } else {
+      // ================================================== e4m3: codes to bf16
+      TreeWalk w;
+      if (KV8 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
+        const int pt = threadIdx.x - 384;
+        const uint32_t raw_base = smem_u32(smem + SM::RAW);
+        int item = 0;
+        bool ok = true;
+        do {
+          const int n = w.n(), len = w.ctx + w.T;
+          for (int u = 0; u < 2 * n && ok; ++u, ++item) {
+            int tile;
+            bool is_v;
+            tree_item(u, n, tile, is_v);
+            const int keys = len - (w.t0 + tile) * 128;  // rows from here on are behind the sequence
+            const int rs = item % TR_RAW, cs = item % ITEMS;
+            ok = mbar_wait(&bars->raw_full[rs], (item / TR_RAW) & 1, p.limit_ns, abort_flag, 851) &&
+                 (item < ITEMS || mbar_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 852));
+            if (!ok) break;
+            convert_tile(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, keys, pt);
+            fence_proxy_async_smem();
+            mbar_arrive(&bars->full[cs]);
+            mbar_arrive(&bars->raw_empty[rs]);
+          }
+        } while (ok && w.next(p));
+      }
+    }
+  }
+
+  // ---- teardown: every role has drained its asynchronous work
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the units that several CTAs share: block (c, y) takes rows
+// 4y .. 4y + 3 (one warp each) of the unit whose first part CTA c holds.
+__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
+  const int c = blockIdx.x;
+  const int4 u = p.part_unit[c];
+  if (u.w < 0) return;
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  int row0, T, ctx;
+  tree_seq(p, u.x, row0, T, ctx);
+  const int t = u.z * p.R + r / p.G;
+  if (r >= p.R * p.G || t >= T) return;
+  // parts in key order: slot 1 of CTA c, then slot 0 of CTAs c + 1 .. last
+  auto slot = [&](int k) { return (static_cast<int64_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * 128 + r; };
+  const int n = u.w - c + 1;
+  float M = -INFINITY;
+  for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[slot(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float2 q = p.part_ml[slot(k)];
+    const float4 v = reinterpret_cast<const float4*>(p.part_o + slot(k) * 128)[lane];
+    const float wt = q.x == -INFINITY ? 0.f : ex2_approx(q.x - M);
+    L = fmaf(q.y, wt, L);
+    acc.x = fmaf(v.x, wt, acc.x);
+    acc.y = fmaf(v.y, wt, acc.y);
+    acc.z = fmaf(v.z, wt, acc.z);
+    acc.w = fmaf(v.w, wt, acc.w);
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int h = u.y * p.G + r % p.G;
+  const int64_t row = row0 + t;
+  *reinterpret_cast<uint2*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + lane * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0 && p.lse)
+    p.lse[static_cast<int64_t>(h) * p.n_tok + row] = (M + log2f(L)) * 0.69314718055994530942f;
+}
+
+}  // namespace hs2

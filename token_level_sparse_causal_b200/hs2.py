@@ -24,7 +24,8 @@ EXPORTS = ("hs2_full_attn_select", "hs2_sparse_attn", "hs2_sync", "hs2_attn_fwd"
            "hs2_topk_select", "hs2_strerror", "hs2_debug_set", "hs2_version", "hs2_launch_count",
            "hs2_full_attn_select_static", "hs2_exp2_check", "hs2_quantize_kv", "hs2_block_select",
            "hs2_full_attn_select_blocks", "hs2_swa_attn", "hs2_sparse_decode",
-           "hs2_sparse_decode_workspace", "hs2_attn_fwd_ws", "hs2_qk_norm_rope", "hs2_cache_evict")
+           "hs2_sparse_decode_workspace", "hs2_attn_fwd_ws", "hs2_qk_norm_rope", "hs2_cache_evict",
+           "hs2_varlen_attn", "hs2_tree_attn", "hs2_tree_attn_workspace", "hs2_cache_weights")
 
 
 class Hs2Shape(ctypes.Structure):
@@ -49,6 +50,20 @@ class Hs2Rope(ctypes.Structure):
                 ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
                 ("kv_tok_stride", ctypes.c_int64), ("kv_head_stride", ctypes.c_int64),
                 ("out_tok_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+class Hs2Varlen(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("total_q", ctypes.c_int32), ("total_k", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("kv_tok_stride", ctypes.c_int64), ("kv_head_stride", ctypes.c_int64)]
+
+
+class Hs2Draft(ctypes.Structure):
+    """hs2_draft: a batch of drafted tokens (make_draft builds it and keeps its tensors alive)."""
+    _fields_ = [("n_tok", ctypes.c_int32), ("max_draft", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("cu_draft", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
 
 
 class Hs2Error(RuntimeError):
@@ -85,6 +100,10 @@ _SIGS = {
     "hs2_qk_norm_rope": [ctypes.POINTER(Hs2Cache), ctypes.POINTER(Hs2Rope), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                          _vp, _vp],
     "hs2_cache_evict": [ctypes.POINTER(Hs2Cache), _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp],
+    "hs2_varlen_attn": [ctypes.POINTER(Hs2Varlen), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "hs2_tree_attn": [ctypes.POINTER(Hs2Cache), ctypes.POINTER(Hs2Draft), _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp],
+    "hs2_tree_attn_workspace": [ctypes.POINTER(Hs2Cache), ctypes.POINTER(Hs2Draft), ctypes.POINTER(ctypes.c_size_t)],
+    "hs2_cache_weights": [ctypes.POINTER(Hs2Cache), ctypes.POINTER(Hs2Draft), _vp, _vp, _vp, _vp, _i64, _vp],
 }
 
 
@@ -348,6 +367,78 @@ def hs2_qk_norm_rope(cache: Hs2Cache, q, k, v, q_weight, k_weight, eps: float, i
                 *_strides(q_out))
     _call("hs2_qk_norm_rope", pool.device, stream, ctypes.byref(cache), ctypes.byref(r), _ptr(q), _ptr(k), _ptr(v),
           _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(slots), _ptr(q_out))
+
+
+def make_varlen(q, k, n_seqs: int) -> Hs2Varlen:
+    """hs2_varlen for packed q [total_q][Hq][128] and k (v alike) [total_k][Hkv][128], bf16."""
+    _need(q, torch.bfloat16, (None, None, 128), "q", False)
+    _need(k, torch.bfloat16, (None, None, 128), "k", False, q)
+    return Hs2Varlen(n_seqs, q.shape[0], k.shape[0], q.shape[1], k.shape[1], 128, *_strides(q), *_strides(k))
+
+
+def hs2_varlen_attn(shape: Hs2Varlen, q, k, v, cu_q, cu_k, o, lse=None, stream=None) -> None:
+    """q, o [total_q][Hq][128], k, v [total_k][Hkv][128]; cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q);
+    lse fp32 [Hq][total_q] or None.  q and o, and k and v, have the strides make_varlen saw."""
+    for t, n, h, st, name in ((q, shape.total_q, shape.Hq, (shape.q_tok_stride, shape.q_head_stride), "q"),
+                              (o, shape.total_q, shape.Hq, (shape.q_tok_stride, shape.q_head_stride), "o"),
+                              (k, shape.total_k, shape.Hkv, (shape.kv_tok_stride, shape.kv_head_stride), "k"),
+                              (v, shape.total_k, shape.Hkv, (shape.kv_tok_stride, shape.kv_head_stride), "v")):
+        _need(t, torch.bfloat16, (n, h, 128), name, False, q)
+        if _strides(t) != st:
+            raise ValueError(f"{name}: strides {_strides(t)}, expected {st}")
+    _need(cu_q, torch.int32, (shape.n_seqs + 1,), "cu_q", True, q)
+    _need(cu_k, torch.int32, (shape.n_seqs + 1,), "cu_k", True, q)
+    _need(lse, torch.float32, (shape.Hq, shape.total_q), "lse", True, q)
+    _call("hs2_varlen_attn", q.device, stream, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k),
+          _ptr(o), _ptr(lse))
+
+
+def make_draft(q, cu_draft, ctx_len, mask, max_draft: int) -> Hs2Draft:
+    """hs2_draft for queries shaped like q [n_tok][Hq][128]; cu_draft int32 [n_seqs + 1], ctx_len int32 [n_seqs],
+    mask int64 or uint64 [n_tok] (None: chains)."""
+    _need(q, torch.bfloat16, (None, None, 128), "q", False)
+    _need(ctx_len, torch.int32, (None,), "ctx_len", True, q)
+    _need(cu_draft, torch.int32, (ctx_len.shape[0] + 1,), "cu_draft", True, q)
+    _need(mask, (torch.int64, torch.uint64), (q.shape[0],), "mask", True, q)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    d = Hs2Draft(q.shape[0], int(max_draft), q.shape[1], 0, *_strides(q), ptr(cu_draft), ptr(ctx_len), ptr(mask))
+    d.tensors = (cu_draft, ctx_len, mask)
+    return d
+
+
+def _need_draft(cache: Hs2Cache, draft: Hs2Draft, q, o=None) -> None:
+    if draft.tensors[1].shape[0] != cache.n_seqs:
+        raise ValueError(f"draft: {draft.tensors[1].shape[0]} sequences, the cache has {cache.n_seqs}")
+    for t, name in ((q, "q"), (o, "o")):
+        if t is not None:
+            _need(t, torch.bfloat16, (draft.n_tok, draft.Hq, 128), name, False, cache.tensors[0])
+            if _strides(t) != (draft.q_tok_stride, draft.q_head_stride):
+                raise ValueError(f"{name}: strides {_strides(t)} are not the draft's")
+
+
+def tree_attn_workspace_bytes(cache: Hs2Cache, draft: Hs2Draft) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().hs2_tree_attn_workspace(ctypes.byref(cache), ctypes.byref(draft), ctypes.byref(n)),
+           "hs2_tree_attn_workspace")
+    return int(n.value)
+
+
+def hs2_tree_attn(cache: Hs2Cache, draft: Hs2Draft, q, o, lse, workspace, stream=None) -> None:
+    """q, o [n_tok][Hq][128] bf16; lse fp32 [Hq][n_tok] or None; workspace of tree_attn_workspace_bytes."""
+    _need_draft(cache, draft, q, o)
+    _need(lse, torch.float32, (draft.Hq, draft.n_tok), "lse", True, q)
+    _call("hs2_tree_attn", q.device, stream, ctypes.byref(cache), ctypes.byref(draft), _ptr(q), _ptr(o), _ptr(lse),
+          _ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def hs2_cache_weights(cache: Hs2Cache, draft: Hs2Draft, q, lse, counted, acc, stream=None) -> None:
+    """lse fp32 [Hq][n_tok] from hs2_tree_attn; counted uint8 [n_tok] or None; acc fp32 [n_seqs][Hkv][acc_stride]."""
+    _need_draft(cache, draft, q)
+    _need(lse, torch.float32, (draft.Hq, draft.n_tok), "lse", True, q)
+    _need(counted, (torch.uint8, torch.bool), (draft.n_tok,), "counted", True, q)
+    _need(acc, torch.float32, (cache.n_seqs, cache.Hkv, None), "acc", True, q)
+    _call("hs2_cache_weights", q.device, stream, ctypes.byref(cache), ctypes.byref(draft), _ptr(q), _ptr(lse),
+          _ptr(counted), _ptr(acc), acc.shape[2])
 
 
 def hs2_cache_evict(cache: Hs2Cache, seq_len, acc, keep: int, recent: int, idx, new_len, acc_out=None,
