@@ -109,7 +109,7 @@ def test_matches_oracle(n, Hq, Hkv, rot, norm, interleaved, kv8):
 
 @pytest.mark.parametrize("kv8", [False, True])
 def test_many_tokens_per_cta(kv8):
-    """Above 8 x 4 tokens per SM a CTA takes four tokens; the last has fewer."""
+    """From 16 tokens per SM on a CTA takes eight tokens; the last has fewer."""
     n = 148 * 32 + 3
     x = _case(n, 2, 1, kv8, 128, True, seed=5)
     _run(x, 2, 1)

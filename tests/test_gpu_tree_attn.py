@@ -72,6 +72,9 @@ CASES = [
     ([500], [64], 16, 1, 64, False),                       # eight tiles of rows
     ([90, 3], [20, 11], 3, 1, 64, True),                   # 42 tokens of 3 heads a tile
     ([4000], [2], 5, 5, 64, True),
+    ([700, 30], [32, 20], 2, 1, 64, True),                 # 64 rows: two blocks of a tile
+    ([600, 129], [10, 2], 9, 3, 64, True),                 # 30 of 32 rows
+    ([260], [21], 3, 1, 16, True),                         # 63 of 64 rows
 ]
 
 
@@ -268,3 +271,36 @@ def test_a_lost_load_times_out(kv8):
         hs2.hs2_debug_set(H.WAIT_LIMIT_NS, 0)
     o, lse, gb = _attend(c)
     _check(c, o, lse, gb)
+
+
+def test_every_e4m3_code_is_converted_exactly():
+    """256 sequences of one drafted token each, so its weight is one: o is the value row, exactly, and lse the score.
+    Sequence b's value row runs through all codes from b on; its key row is code b everywhere and its query a one
+    in one dimension.  The two NaN codes stay NaN."""
+    import math
+    from oracle import hs2_oracle as orc
+    codes = torch.arange(256)
+    v = ((codes[:, None] + codes[None, :128]) % 256).to(torch.uint8)
+    pool = lambda rows: torch.zeros(256 * 16, 1, 128, dtype=torch.uint8).index_copy_(
+        0, 16 * codes, rows.view(256, 1, 128)).to(DEV)
+    k = codes.to(torch.uint8).view(256, 1).expand(256, 128).contiguous()
+    q = torch.zeros(256, 1, 128, dtype=torch.bfloat16)
+    q[codes, 0, codes % 128] = 1
+    one = torch.ones(256 * 16, 1, device=DEV)
+    cache = hs2.make_cache(pool(k), pool(v), codes.to(torch.int32).view(256, 1).to(DEV), 16, one, one)
+    q = q.to(DEV)
+    draft = hs2.make_draft(q, torch.arange(257, dtype=torch.int32, device=DEV),
+                           torch.zeros(256, dtype=torch.int32, device=DEV), None, 1)
+    o, lse = torch.empty_like(q), torch.empty(1, 256, device=DEV)
+    ws = torch.empty(hs2.tree_attn_workspace_bytes(cache, draft), dtype=torch.uint8, device=DEV)
+    hs2.hs2_tree_attn(cache, draft, q, o, lse, ws)
+    hs2.hs2_sync()
+    value = orc.decode_e4m3(np.arange(256, dtype=np.uint8))
+    finite = np.isfinite(value)
+    assert (~finite).sum() == 2
+    good = [b for b in range(256) if finite[b]]      # a NaN score leaves no weight to speak of
+    assert np.array_equal(f64(o[good, 0]), value[v.numpy()[good]], equal_nan=True)
+    # a key of one code adds up 127 zeros and itself: the score is that value times 1/sqrt(128), rounded
+    got = lse[0].double().cpu().numpy()
+    assert np.isnan(got[~finite]).all() and torch.isnan(o.cpu()[~finite]).all()
+    assert (np.abs(got[good] - value[good] / math.sqrt(128)) <= 2.0 ** -20 * np.abs(value[good])).all()

@@ -32,31 +32,40 @@ __device__ __forceinline__ void mask_after(uint32_t (&sr)[4][32], int last) {
     if (c > last) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
 }
 
-// P of the tile over the scores' first 64 columns; returns whether this row's
-// O has to be multiplied by alpha.  With a V scale per key (VSCALE) P times
-// the scale is what is rounded; the sum is of P.
-template <bool VSCALE>
-__device__ __forceinline__ bool softmax_tile(uint32_t s_tm, const uint32_t (&sr)[4][32], float sc,
-                                             const float* vscale, RowState& st, float& alpha) {
-  float mx8[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint32_t* v = &sr[q >> 1][(q & 1) * 16];
-    float m = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-#pragma unroll
-    for (int e = 0; e < 6; ++e) m = fmax3(m, __uint_as_float(v[3 + 2 * e]), __uint_as_float(v[4 + 2 * e]));
-    mx8[q] = fmaxf(m, __uint_as_float(v[15]));
-  }
-  const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-  const float m_new = fmaxf(st.m, mx * sc);
+// Moves the reference max to a row max of `mx` (scaled) where that grew by more
+// than 8; returns whether, with what l and O have to be multiplied by.
+__device__ __forceinline__ bool update_max(float mx, RowState& st, float& alpha) {
+  const float m_new = fmaxf(st.m, mx);
   alpha = 1.f;
   const bool resc = m_new > st.m + 8.f;
   if (resc) {
     alpha = ex2_approx(st.m - m_new);
     st.m = m_new;
   }
-  const float mu = (st.m == -INFINITY) ? 0.f : st.m;
   st.l *= alpha;
+  return resc;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+  float mx2[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t* u = &v[q * 16];
+    float m = fmax3(__uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2]));
+#pragma unroll
+    for (int e = 0; e < 6; ++e) m = fmax3(m, __uint_as_float(u[3 + 2 * e]), __uint_as_float(u[4 + 2 * e]));
+    mx2[q] = fmaxf(m, __uint_as_float(u[15]));
+  }
+  return fmaxf(mx2[0], mx2[1]);
+}
+
+// P of a tile with its row in registers, over the scores' first 64 columns;
+// returns whether this row's O has to be multiplied by alpha.
+__device__ __forceinline__ bool softmax_tile(uint32_t s_tm, const uint32_t (&sr)[4][32], float sc, RowState& st,
+                                             float& alpha) {
+  const float mx = fmaxf(fmaxf(max32(sr[0]), max32(sr[1])), fmaxf(max32(sr[2]), max32(sr[3])));
+  const bool resc = update_max(mx * sc, st, alpha);
+  const float mu = (st.m == -INFINITY) ? 0.f : st.m;
   const uint64_t sc2 = f2_pack(sc, sc), nmu2 = f2_pack(-mu, -mu);
   uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
@@ -66,14 +75,106 @@ __device__ __forceinline__ bool softmax_tile(uint32_t s_tm, const uint32_t (&sr)
     for (int e = 0; e < 16; ++e) {
       const uint64_t a2 =
           f2_fma(f2_pack(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1])), sc2, nmu2);
-      uint64_t p2 = ex2_x2(a2);
+      const uint64_t p2 = ex2_x2(a2);
       sum2[e & 1] = f2_add(sum2[e & 1], p2);
-      if (VSCALE) p2 = f2_mul(p2, reinterpret_cast<const uint64_t*>(vscale)[c * 16 + e]);
       float e0, e1;
       f2_unpack(p2, e0, e1);
       pk[e] = pack_bf16x2(e0, e1);
     }
     tmem_st16(s_tm + c * 16, pk);
+  }
+  float a0, a1, b0, b1;
+  f2_unpack(sum2[0], a0, a1);
+  f2_unpack(sum2[1], b0, b1);
+  st.l += (a0 + a1) + (b0 + b1);
+  return resc;
+}
+
+// The same for NQ quarters (32 columns each) of a tile from quarter q0 on, the
+// other columns' P set to zero; optionally (SCALED) with a K and a V scale per
+// key in shared memory ([128] each: scores are multiplied by the K scale, and P
+// times the V scale is what is rounded, the sum is of P), and with a mask of
+// visible columns (4 words).  The scores are read from tensor memory twice, a
+// quarter ahead of its use, so that a row takes 64 registers, not 128.
+template <int NQ, bool SCALED>
+__device__ __forceinline__ bool softmax_quarters(uint32_t s_tm, int q0, float sc, const float* kscale,
+                                                 const float* vscale, bool masked, const uint32_t (&vis)[4],
+                                                 RowState& st, float& alpha) {
+  uint32_t buf[2][32];
+  auto issue = [&](int q) { tmem_ld32(s_tm + 32 * (q0 + q), buf[q & 1]); };
+  auto arrived = [&](int q) {
+    tmem_ld_wait();
+    reg_fence(buf[q & 1]);
+  };
+  // scores of quarter q as they enter the softmax
+  auto prepare = [&](int q) {
+    uint32_t(&sr)[32] = buf[q & 1];
+    if (SCALED) {
+      const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(kscale + 32 * (q0 + q));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const ulonglong2 k2 = ks[e];  // broadcast
+        float a0, a1, a2, a3;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(sr[4 * e]), __uint_as_float(sr[4 * e + 1])), k2.x), a0, a1);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(sr[4 * e + 2]), __uint_as_float(sr[4 * e + 3])), k2.y), a2, a3);
+        sr[4 * e] = __float_as_uint(a0);
+        sr[4 * e + 1] = __float_as_uint(a1);
+        sr[4 * e + 2] = __float_as_uint(a2);
+        sr[4 * e + 3] = __float_as_uint(a3);
+      }
+    }
+    if (masked) {
+      const uint32_t w = NQ == 4 ? vis[q] : (q0 + q < 2 ? (q0 + q ? vis[1] : vis[0]) : (q0 + q == 2 ? vis[2] : vis[3]));
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!(w >> e & 1u)) sr[e] = __float_as_uint(-INFINITY);
+    }
+  };
+  float mx = -INFINITY;
+  issue(0);
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    arrived(q);
+    if (q + 1 < NQ) issue(q + 1);
+    prepare(q);
+    mx = fmaxf(mx, max32(buf[q & 1]));
+    if (NQ > 2 && q + 1 == NQ) issue(0);  // quarter 0 again; NQ <= 2: all are still in registers
+  }
+  const bool resc = update_max(mx * sc, st, alpha);
+  const float mu = (st.m == -INFINITY) ? 0.f : st.m;
+  const uint64_t sc2 = f2_pack(sc, sc), nmu2 = f2_pack(-mu, -mu);
+  uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    if (NQ > 2) {
+      arrived(q);
+      if (q + 1 < NQ) issue(q + 1);
+      prepare(q);
+    }
+    const uint32_t(&sr)[32] = buf[q & 1];
+    const ulonglong2* vs = reinterpret_cast<const ulonglong2*>(vscale + 32 * (q0 + q));
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t a2 = f2_fma(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sc2, nmu2);
+      uint64_t p2 = ex2_x2(a2);
+      sum2[e & 1] = f2_add(sum2[e & 1], p2);
+      if (SCALED) p2 = f2_mul(p2, (e & 1) ? vs[e >> 1].y : vs[e >> 1].x);
+      float e0, e1;
+      f2_unpack(p2, e0, e1);
+      pk[e] = pack_bf16x2(e0, e1);
+    }
+    // over scores that this thread has read for the last time: quarter q + 1,
+    // on its way to registers, lies behind column 16 (q + 1)
+    tmem_st16(s_tm + (q0 + q) * 16, pk);
+  }
+  if (NQ < 4) {
+    uint32_t zero[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zero[e] = 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < q0 || q >= q0 + NQ) tmem_st16(s_tm + q * 16, zero);
   }
   float a0, a1, b0, b1;
   f2_unpack(sum2[0], a0, a1);

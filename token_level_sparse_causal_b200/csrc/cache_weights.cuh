@@ -17,7 +17,7 @@
 // and SM).  Exponentials run on the MUFU unit (2^-22): the cubic polynomial
 // that kernel (2) mixes in is exact only to 7.5e-5.
 //
-// e4m3: codes arrive by TMA in a raw ring and are turned into bf16 by four
+// e4m3: codes arrive by TMA in a raw ring and are turned into bf16 by eight
 // warps; the key's scale multiplies its row of scores.
 #pragma once
 
@@ -44,8 +44,9 @@ struct WeightBars {
   uint64_t s_full[2], s_empty[2];
   uint64_t rows_ready[2];
   uint64_t fin;
-  int64_t first, count;
-  int b, g, tile;
+  int first, count;   // as in TreeBars; a unit is a (sequence, KV head) here
+  int b, unit, tile;
+  int each, more;
   uint32_t tmem_slot;
   int abort;
 };
@@ -68,7 +69,7 @@ struct WeightSmem {
 // token tile m); all token tiles of a key range come one after another.
 struct WeightWalk {
   int b, g, m, row0, T, ctx, tiles, mtiles, t0, t1;
-  int64_t left;
+  int left;
   __device__ __forceinline__ void load(const TreeParams& p) {
     tree_seq(p, b, row0, T, ctx);
     tiles = T ? (ctx + T + 127) >> 7 : 0;
@@ -78,11 +79,11 @@ struct WeightWalk {
     left = bars->count;
     if (left <= 0) return false;
     b = bars->b;
-    g = bars->g;
+    g = bars->unit;
     m = 0;
     load(p);
     t0 = bars->tile;
-    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + left));
+    t1 = min(tiles, t0 + left);
     return true;
   }
   __device__ __forceinline__ bool next(const TreeParams& p) {
@@ -98,53 +99,11 @@ struct WeightWalk {
       } while (T == 0);
     }
     t0 = 0;
-    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+    t1 = min(tiles, left);
     return true;
   }
   __device__ __forceinline__ int n() const { return t1 - t0; }
 };
-
-__device__ __forceinline__ void weights_split(const TreeParams& p, WeightBars* bars) {
-  const int lane = threadIdx.x & 31;
-  auto cost = [&](int b) -> int64_t {
-    if (b >= p.B) return 0;
-    int row0, T, ctx;
-    if (!tree_seq(p, b, row0, T, ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, 901);
-    return T ? static_cast<int64_t>((ctx + T + 127) >> 7) * p.Hkv : 0;
-  };
-  int64_t total = 0;
-  for (int b = lane; b < p.B; b += 32) total += cost(b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int64_t first = blockIdx.x * total / gridDim.x;
-  const int64_t count = (blockIdx.x + 1) * total / gridDim.x - first;
-  if (lane == 0) {
-    bars->first = first;
-    bars->count = count;
-  }
-  if (count == 0) return;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int64_t w = cost(b0 + lane), incl = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const bool here = first >= before + incl - w && first < before + incl;
-    if (here) {
-      int row0, T, ctx;
-      tree_seq(p, b0 + lane, row0, T, ctx);
-      const int tiles = (ctx + T + 127) >> 7;
-      const int64_t rest = first - (before + incl - w);
-      bars->b = b0 + lane;
-      bars->g = static_cast<int>(rest / tiles);
-      bars->tile = static_cast<int>(rest % tiles);
-    }
-    if (__any_sync(0xffffffffu, here)) return;
-    before += __shfl_sync(0xffffffffu, incl, 31);
-  }
-}
 
 template <bool KV8>
 __global__ void __launch_bounds__(tr_threads(KV8), 1)
@@ -166,13 +125,13 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ITEMS; ++s) {
-      mbar_init(&bars->full[s], KV8 ? 128u : 1u);
+      mbar_init(&bars->full[s], KV8 ? TR_CONV / 32 : 1);
       mbar_init(&bars->empty[s], 1);
     }
     if (KV8) {
       for (int s = 0; s < CW_RAW; ++s) {
         mbar_init(&bars->raw_full[s], 1);
-        mbar_init(&bars->raw_empty[s], 128);
+        mbar_init(&bars->raw_empty[s], TR_CONV / 32);
       }
     }
     mbar_init(&bars->q_full, 1);
@@ -192,7 +151,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     tmem_alloc(&bars->tmem_slot, 256);
     tmem_relinquish();
   }
-  if (warp == 2) weights_split(p, bars);
+  if (warp == 2) tree_split(p, bars, false, 901);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -335,19 +294,31 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       const int len = w.ctx + w.T, n = w.n();
       const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
       float* acc = wp.acc + (static_cast<int64_t>(w.b) * p.Hkv + w.g) * wp.acc_stride;
+      // this thread's key of tile j: the sum so far and (e4m3) the page, both
+      // read before they are needed: the sum and the scale one tile of this
+      // warpgroup ahead, the page two
+      auto page_of = [&](int j) {
+        const int at = (w.t0 + j) * 128 + r;
+        return KV8 && j < n && at < len ? table[at >> p.page_log2] : -1;
+      };
+      auto fetch = [&](int j, int pg, float& old, float& f) {
+        const int at = (w.t0 + j) * 128 + r;
+        old = j < n && at < len ? acc[at] : 0.f;
+        f = p.scale_log2;
+        if (KV8) {
+          f = 0.f;  // a page outside the pools reads as zeros
+          if (pg >= 0 && pg < p.n_pages)
+            f = p.ksc[((static_cast<int64_t>(pg) << p.page_log2) + (at & ((1 << p.page_log2) - 1))) * p.Hkv + w.g];
+        }
+      };
+      float old_next, f_next;
+      fetch(x, page_of(x), old_next, f_next);
+      int pg_next = page_of(x + 2);
       for (int j = x; j < n; j += 2, ++ns) {
         const int at = (w.t0 + j) * 128 + r;
-        float old = 0.f, f = p.scale_log2;
-        if (at < len) {
-          old = acc[at];
-          if (KV8) {
-            const int pg = table[at >> p.page_log2];
-            f = 0.f;
-            if (pg >= 0 && pg < p.n_pages)
-              f = p.scale_log2 * p.ksc[((static_cast<int64_t>(pg) << p.page_log2) + (at & ((1 << p.page_log2) - 1))) *
-                                           p.Hkv + w.g];
-          }
-        }
+        const float old = old_next, f = KV8 ? f_next * p.scale_log2 : f_next;
+        fetch(j + 2, pg_next, old_next, f_next);
+        pg_next = page_of(j + 4);
         if (!(ok = warp_wait(&bars->s_full[x], ns & 1, p.limit_ns, abort_flag, 941))) break;
         tc_fence_after();
         const int d = at - w.ctx;  // >= 0: a drafted key
@@ -395,13 +366,16 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       do {
         for (int t = w.t0; t < w.t1 && ok; ++t, ++item) {
           const int rs = item % CW_RAW, cs = item % ITEMS;
-          ok = mbar_wait(&bars->raw_full[rs], (item / CW_RAW) & 1, p.limit_ns, abort_flag, 951) &&
-               (item < ITEMS || mbar_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 952));
+          ok = warp_wait(&bars->raw_full[rs], (item / CW_RAW) & 1, p.limit_ns, abort_flag, 951) &&
+               (item < ITEMS || warp_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 952));
           if (!ok) break;
           convert_tile(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, w.ctx + w.T - t * 128, pt);
           fence_proxy_async_smem();
-          mbar_arrive(&bars->full[cs]);
-          mbar_arrive(&bars->raw_empty[rs]);
+          __syncwarp();  // one arrival per warp: 256 of them would take longer than the conversion
+          if (lane == 0) {
+            mbar_arrive(&bars->full[cs]);
+            mbar_arrive(&bars->raw_empty[rs]);
+          }
         }
       } while (ok && w.next(p));
     }

@@ -2,22 +2,21 @@
 // and KV head the keep - recent heaviest positions of [0, n - recent) (ties to
 // the lower position) and the last `recent`, moved to positions 0 .. keep - 1.
 //
-// One cluster of EV_CTAS CTAs per (sequence, KV head).  Bound by memory (the
-// row of weights is read once, the kept K and V rows are read and written
-// once) and, for few rows, by the latency of its steps.
+// One cluster of CTAs per (sequence, KV head).  Bound by memory (the row of
+// weights is read once, the kept K and V rows are read and written once) and,
+// for few rows, by the latency of its steps.
 //   select   each CTA holds its contiguous part of the row as order-preserving
 //            32-bit keys in shared memory (parts too long for it are read from
 //            global memory again) and the cluster finds the k-th largest key
-//            by a radix search of 11 + 11 + 10 bits: a histogram per CTA,
-//            added up through distributed shared memory;
+//            by a radix search of 11 + 11 + 10 bits: a histogram per CTA and
+//            pass, added up through distributed shared memory;
 //   list     a CTA's warps own contiguous pieces of its part; counts of larger
 //            and equal keys before each piece (over the cluster, then over the
 //            CTA) give every kept position its place, so the list comes out
 //            ascending without a sort;
-//   move     CTA r moves one slice of the columns, 1 / EV_CTAS of a K and V
-//            row, through the whole list in ascending order.  The new place of
-//            a row is never behind its old one, so once a batch of rows is in
-//            registers (one barrier) it can be stored without touching a row
+//   move     the cluster takes the list in ascending batches.  The new place of
+//            a row is never behind its old one, so once a batch is in registers
+//            (one cluster barrier) it can be stored without touching a row
 //            that a later batch reads: the move needs no second buffer.
 #pragma once
 
@@ -29,9 +28,9 @@
 namespace hs2 {
 
 constexpr int EV_THREADS = 512;
-constexpr int EV_CTAS = 8;      // CTAs of a cluster
+constexpr int EV_MAX_CTAS = 16;  // CTAs of a cluster
 constexpr int EV_BINS = 2048;
-constexpr int EV_ROWS = 8;      // row pieces in flight per thread
+constexpr int EV_ROWS = 8;      // 16-byte pieces in flight per thread
 constexpr int EV_MAX_PART = 40960;  // keys a CTA holds in shared memory
 static_assert(EV_THREADS == SEL_THREADS, "block_excl_scan");
 
@@ -48,7 +47,7 @@ struct EvictParams {
 };
 
 struct EvictSmem {
-  uint32_t hist[2][EV_BINS];  // this CTA's counts, then the cluster's
+  uint32_t hist[3][EV_BINS];  // this CTA's counts of each pass, read by the other CTAs
   uint32_t warp_gt[16], warp_eq[16];
   uint32_t cta_gt, cta_eq;    // read by the other CTAs
   uint32_t scan[16];
@@ -57,13 +56,13 @@ struct EvictSmem {
 };
 
 template <bool KV8>
-__global__ void __cluster_dims__(EV_CTAS, 1, 1) __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ __align__(16) uint8_t ev_raw[];
   EvictSmem& sm = *reinterpret_cast<EvictSmem*>(ev_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(cl.block_rank());
+  const int rank = static_cast<int>(cl.block_rank()), ctas = static_cast<int>(cl.num_blocks());
   const int g = blockIdx.y, b = blockIdx.z;
   const int64_t row = static_cast<int64_t>(b) * p.Hkv + g;
   const int n = p.len[b];
@@ -78,15 +77,15 @@ __global__ void __cluster_dims__(EV_CTAS, 1, 1) __launch_bounds__(EV_THREADS) ca
   }
   if (rank == 0 && g == 0 && tid == 0) p.new_len[b] = min(n, p.keep);
   if (n <= p.keep) {
-    for (int i = rank * EV_THREADS + tid; i < p.keep; i += EV_CTAS * EV_THREADS) idx[i] = i < n ? i : -1;
+    for (int i = rank * EV_THREADS + tid; i < p.keep; i += ctas * EV_THREADS) idx[i] = i < n ? i : -1;
     if (acc_out && acc_out != acc)
-      for (int i = rank * EV_THREADS + tid; i < n; i += EV_CTAS * EV_THREADS) acc_out[i] = acc[i];
+      for (int i = rank * EV_THREADS + tid; i < n; i += ctas * EV_THREADS) acc_out[i] = acc[i];
     return;
   }
 
   // ---- select: the k-th largest key of the candidates
   const int n_c = n - p.recent, k = p.keep - p.recent;  // n_c > k >= 0
-  const int part = ((n_c + EV_CTAS - 1) / EV_CTAS + 3) & ~3;
+  const int part = ((n_c + ctas - 1) / ctas + 3) & ~3;
   const int lo = min(n_c, rank * part), cnt = min(n_c, lo + part) - lo;
   const bool held = part <= p.part_cap;
   auto key_at = [&](int i) { return held ? sm.keys[i] : order_key(acc[lo + i]); };
@@ -100,51 +99,49 @@ __global__ void __cluster_dims__(EV_CTAS, 1, 1) __launch_bounds__(EV_THREADS) ca
             make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
       }
     }
+    for (int i = tid; i < 3 * EV_BINS / 4; i += EV_THREADS)
+      reinterpret_cast<uint4*>(sm.hist[0])[i] = make_uint4(0, 0, 0, 0);
     uint32_t prefix = 0, pmask = 0;
     krem = static_cast<uint32_t>(k);
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t dmask = pass == 2 ? 1023u : 2047u;
-      const int bins = static_cast<int>(dmask) + 1;
-      for (int i = tid; i < bins; i += EV_THREADS) sm.hist[0][i] = 0;
+      uint32_t* hist = sm.hist[pass];
       __syncthreads();
       for (int i = tid; i < cnt; i += EV_THREADS) {
         const uint32_t key = key_at(i);
-        if ((key & pmask) == prefix) atomicAdd(&sm.hist[0][(key >> shift) & dmask], 1u);
+        if ((key & pmask) == prefix) atomicAdd(&hist[(key >> shift) & dmask], 1u);
       }
-      cl.sync();
-      for (int i = tid; i < bins; i += EV_THREADS) {
-        uint32_t c = 0;
-#pragma unroll
-        for (int r = 0; r < EV_CTAS; ++r) c += cl.map_shared_rank(sm.hist[0], r)[i];
-        sm.hist[1][i] = c;
+      cl.sync();  // each pass has counts of its own, so one barrier a pass is enough
+      // thread t owns four bins, from the top down (the last pass fills the lower half only)
+      const int bin0 = EV_BINS - 4 * (tid + 1);
+      uint32_t c[4] = {0, 0, 0, 0};
+      for (int r = 0; r < ctas; ++r) {
+        const uint4 x = reinterpret_cast<const uint4*>(cl.map_shared_rank(hist, r))[bin0 >> 2];
+        c[0] += x.x;
+        c[1] += x.y;
+        c[2] += x.z;
+        c[3] += x.w;
       }
-      cl.sync();  // every CTA has read the others' counts
-      // thread t owns bins from the top down; find the one that holds rank krem
-      const int per = bins / EV_THREADS;
-      uint32_t loc = 0;
-      for (int q = 0; q < per; ++q) loc += sm.hist[1][bins - 1 - (tid * per + q)];
       uint32_t tot;
+      const uint32_t loc = (c[0] + c[1]) + (c[2] + c[3]);
       const uint32_t ex = block_excl_scan(loc, sm.scan, &tot);
       if (ex < krem && ex + loc >= krem) {
         uint32_t run = ex;
-        for (int q = 0; q < per; ++q) {
-          const int bin = bins - 1 - (tid * per + q);
-          const uint32_t c = sm.hist[1][bin];
-          if (run + c >= krem) {
-            sm.sh[0] = static_cast<uint32_t>(bin);
+#pragma unroll
+        for (int q = 3; q >= 0; --q) {
+          if (run < krem && run + c[q] >= krem) {
+            sm.sh[0] = static_cast<uint32_t>(bin0 + q);
             sm.sh[1] = run;
-            break;
           }
-          run += c;
+          run += c[q];
         }
       }
       __syncthreads();
       prefix |= sm.sh[0] << shift;
       pmask |= dmask << shift;
       krem -= sm.sh[1];
-      __syncthreads();
     }
     T = prefix;
 
@@ -196,16 +193,12 @@ __global__ void __cluster_dims__(EV_CTAS, 1, 1) __launch_bounds__(EV_THREADS) ca
       eq_before += __popc(me);
     }
   }
-  if (rank == EV_CTAS - 1)
+  if (rank == ctas - 1)
     for (int i = tid; i < p.recent; i += EV_THREADS) idx[k + i] = n - p.recent + i;
   cl.sync();  // the list is complete; no CTA reads another's shared memory any more
 
-  // ---- move: this CTA's slice of the columns, in ascending order
-  constexpr int SLICE = KV8 ? 32 : 64;        // bytes of a row
-  constexpr int LANES = SLICE / 16;           // threads per row piece
-  constexpr int STEP = EV_THREADS / LANES;    // rows per step
-  const int64_t col = static_cast<int64_t>(rank % (EV_CTAS / 2)) * SLICE + (tid % LANES) * 16;
-  uint8_t* base = (rank < EV_CTAS / 2 ? p.k : p.v) + static_cast<int64_t>(g) * p.head_b + col;
+  // ---- move: batches of rows, in ascending order, by the whole cluster
+  constexpr int PIECES = KV8 ? 16 : 32;  // 16-byte pieces of a K row and a V row
   const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages;
   // token of the pools that holds position pos, or -1
   auto token_of = [&](int pos) -> int64_t {
@@ -216,54 +209,59 @@ __global__ void __cluster_dims__(EV_CTAS, 1, 1) __launch_bounds__(EV_THREADS) ca
     }
     return (static_cast<int64_t>(pg) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
   };
-  for (int i0 = 0; i0 < p.keep; i0 += STEP * EV_ROWS) {
-    uint4 piece[EV_ROWS];
+  const int piece = tid % PIECES;
+  uint8_t* base = (piece < PIECES / 2 ? p.k : p.v) + static_cast<int64_t>(g) * p.head_b + (piece % (PIECES / 2)) * 16;
+  const int step = ctas * (EV_THREADS / PIECES);  // rows the cluster's threads cover at once
+  const int row0 = rank * (EV_THREADS / PIECES) + tid / PIECES;
+  const int batch = step * EV_ROWS;
+  const int ctid = rank * EV_THREADS + tid;  // scalars of row ctid of a batch
+  for (int i0 = 0; i0 < p.keep; i0 += batch) {
+    uint4 data[EV_ROWS];
     bool have[EV_ROWS];
 #pragma unroll
     for (int e = 0; e < EV_ROWS; ++e) {
-      const int i = i0 + e * STEP + tid / LANES;
+      const int i = i0 + e * step + row0;
       have[e] = false;
       if (i < p.keep) {
         const int64_t tok = token_of(idx[i]);
         have[e] = tok >= 0;
-        if (have[e]) piece[e] = *reinterpret_cast<const uint4*>(base + tok * p.tok_b);
+        if (have[e]) data[e] = *reinterpret_cast<const uint4*>(base + tok * p.tok_b);
       }
     }
-    __syncthreads();
+    float x_acc = 0.f, x_ks = 0.f, x_vs = 0.f;
+    int64_t from = -1;
+    const int is = i0 + ctid;
+    const bool scalar = ctid < batch && is < p.keep;
+    if (scalar) {
+      const int old = idx[is];
+      x_acc = acc[old];
+      if (KV8 && (from = token_of(old)) >= 0) {
+        x_ks = p.ksc[from * p.Hkv + g];
+        x_vs = p.vsc[from * p.Hkv + g];
+      }
+    }
+    cl.sync();  // the batch is in registers
 #pragma unroll
     for (int e = 0; e < EV_ROWS; ++e) {
-      const int i = i0 + e * STEP + tid / LANES;
       if (have[e]) {
-        const int64_t tok = token_of(i);
-        if (tok >= 0) *reinterpret_cast<uint4*>(base + tok * p.tok_b) = piece[e];
+        const int64_t tok = token_of(i0 + e * step + row0);
+        if (tok >= 0) *reinterpret_cast<uint4*>(base + tok * p.tok_b) = data[e];
+      }
+    }
+    if (scalar) {
+      if (acc_out) acc_out[is] = x_acc;
+      if (KV8 && from >= 0) {
+        const int64_t to = token_of(is);
+        if (to >= 0) {
+          p.ksc[to * p.Hkv + g] = x_ks;
+          p.vsc[to * p.Hkv + g] = x_vs;
+        }
       }
     }
   }
-  // scales and weights, one array a CTA, the same way
-  float* sc = !KV8 ? nullptr : rank == 1 ? p.ksc : rank == 2 ? p.vsc : nullptr;
-  if (sc) {
-    for (int i0 = 0; i0 < p.keep; i0 += EV_THREADS) {
-      const int i = i0 + tid;
-      int64_t from = -1;
-      float x = 0.f;
-      if (i < p.keep && (from = token_of(idx[i])) >= 0) x = sc[from * p.Hkv + g];
-      __syncthreads();
-      if (from >= 0) {
-        const int64_t to = token_of(i);
-        if (to >= 0) sc[to * p.Hkv + g] = x;
-      }
-    }
-  }
-  if (rank == 0 && acc_out) {
-    for (int i0 = 0; i0 < p.keep; i0 += EV_THREADS) {
-      const int i = i0 + tid;
-      const float x = i < p.keep ? acc[idx[i]] : 0.f;
-      __syncthreads();
-      if (i < p.keep) acc_out[i] = x;
-    }
-    __syncthreads();  // acc_out may be acc: every kept weight is read
-    for (int i = p.keep + tid; i < n; i += EV_THREADS) acc_out[i] = 0.f;
-  }
+  // acc_out may be acc: every kept weight is read by now
+  if (acc_out)
+    for (int i = p.keep + ctid; i < n; i += ctas * EV_THREADS) acc_out[i] = 0.f;
 }
 
 }  // namespace hs2

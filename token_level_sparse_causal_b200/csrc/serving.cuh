@@ -94,13 +94,14 @@ int check_draft(const hs2_cache* c, const hs2_draft* d) {
   return HS2_OK;
 }
 
-TreeParams tree_params(const hs2_cache* c, const hs2_draft* d) {
+// rows: of a token tile (query rows of one KV head)
+TreeParams tree_params(const hs2_cache* c, const hs2_draft* d, int rows) {
   TreeParams p{};
   p.B = c->n_seqs;
   p.Hq = d->Hq;
   p.Hkv = c->Hkv;
   p.G = d->Hq / c->Hkv;
-  p.R = 128 / p.G;
+  p.R = rows / p.G;
   p.page_log2 = log2_of(c->page);
   p.n_pages = c->n_pages;
   p.max_pages = c->max_pages;
@@ -134,10 +135,69 @@ TreePlan tree_plan() {
   return t;
 }
 
-template <bool KV8, bool PAIRS>
-int launch_norm_rope(const NormRopeParams& p, dim3 grid, cudaStream_t st) {
+template <int TOK>
+int launch_norm_rope(const NormRopeParams& p, bool kv8, bool pairs, cudaStream_t st) {
   const Range range("hs2 qk_norm_rope");
-  qk_norm_rope_kernel<KV8, PAIRS><<<grid, NR_THREADS, 0, st>>>(p);
+  const unsigned grid = static_cast<unsigned>((p.n + TOK - 1) / TOK);
+  if (kv8 && pairs)
+    qk_norm_rope_kernel<true, true, TOK><<<grid, NR_THREADS, 0, st>>>(p);
+  else if (kv8)
+    qk_norm_rope_kernel<true, false, TOK><<<grid, NR_THREADS, 0, st>>>(p);
+  else if (pairs)
+    qk_norm_rope_kernel<false, true, TOK><<<grid, NR_THREADS, 0, st>>>(p);
+  else
+    qk_norm_rope_kernel<false, false, TOK><<<grid, NR_THREADS, 0, st>>>(p);
+  return launched();
+}
+
+template <typename K>
+int launch_evict(K kernel, const EvictParams& p, const hs2_cache* c, int ctas, uint32_t smem, cudaStream_t st) {
+  if (int rc = set_smem(kernel, smem)) return rc;
+  if (ctas > 8) {  // a cluster of 16 is allowed kernel by kernel
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return HS2_ERR_CUDA;
+  }
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(c->n_seqs));
+  cfg.blockDim = dim3(EV_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return HS2_ERR_CUDA;
+  }
+  return launched();
+}
+
+// The attention, then the join of split units; the second kernel's launch
+// overlaps the first one's run (it waits on the device for its end).
+template <bool KV8, int RB>
+int launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TreeParams& p, int ctas,
+                int most_rows, cudaStream_t st) {
+  constexpr uint32_t smem = TreeSmem<KV8, RB>::BYTES;
+  if (int rc = set_smem(tree_attn_kernel<KV8, RB>, smem)) return rc;
+  tree_attn_kernel<KV8, RB><<<static_cast<unsigned>(ctas), tr_threads(KV8), smem, st>>>(mq, mk, mv, p);
+  if (int rc = launched()) return rc;
+  const int rows = std::min(p.R * p.G, most_rows);  // of a unit
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, tree_merge_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return HS2_ERR_CUDA;
+  }
   return launched();
 }
 
@@ -167,7 +227,7 @@ int hs2_qk_norm_rope(const hs2_cache* cache, const hs2_rope* rope, const void* q
   if (!q || !k || !v || !inv_freq || !positions || !q_out) return HS2_ERR_INVALID_ARG;
   if ((q_weight == nullptr) != (k_weight == nullptr)) return HS2_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out)) return HS2_ERR_UNSUPPORTED;
-  if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) & 1u) return HS2_ERR_UNSUPPORTED;
+  if (!aligned16(q_weight) || !aligned16(k_weight)) return HS2_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(inv_freq) & 7u) ||
       ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 3u))
     return HS2_ERR_UNSUPPORTED;
@@ -202,13 +262,10 @@ int hs2_qk_norm_rope(const hs2_cache* cache, const hs2_rope* rope, const void* q
   p.c_tok = cache->tok_stride;
   p.c_head = cache->head_stride;
   p.n_slots = static_cast<int64_t>(cache->n_pages) * cache->page;
-  // one token a CTA until that fills the GPU several times over
-  p.tok_per_cta = p.n >= sm_count() * 8 * NR_MAX_TOK ? NR_MAX_TOK : 1;
-  const dim3 grid(static_cast<unsigned>((p.n + p.tok_per_cta - 1) / p.tok_per_cta));
+  // a CTA per token until that fills the GPU a few times over, then a warp per token
+  const bool kv8 = cache->kv_dtype == HS2_KV_E4M3, pairs = rope->interleaved != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->kv_dtype == HS2_KV_E4M3)
-    return rope->interleaved ? launch_norm_rope<true, true>(p, grid, st) : launch_norm_rope<true, false>(p, grid, st);
-  return rope->interleaved ? launch_norm_rope<false, true>(p, grid, st) : launch_norm_rope<false, false>(p, grid, st);
+  return p.n >= sm_count() * 16 ? launch_norm_rope<8>(p, kv8, pairs, st) : launch_norm_rope<1>(p, kv8, pairs, st);
 }
 
 int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float* acc, float* acc_out,
@@ -244,22 +301,18 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   p.acc_stride = acc_stride;
   p.idx = idx;
   p.new_len = new_len;
+  // CTAs a row: as many as keep every SM busy, up to the largest cluster
+  const int64_t rows = static_cast<int64_t>(cache->n_seqs) * cache->Hkv;
+  int ctas = EV_MAX_CTAS;
+  while (ctas > 1 && rows * ctas > 4 * sm_count()) ctas /= 2;
   // shared memory for the longest part a row of this cache can have
   const int64_t longest = std::min<int64_t>(acc_stride, static_cast<int64_t>(cache->max_pages) * cache->page);
-  const int64_t part = ((longest + EV_CTAS - 1) / EV_CTAS + 3) & ~int64_t(3);
+  const int64_t part = ((longest + ctas - 1) / ctas + 3) & ~int64_t(3);
   p.part_cap = static_cast<int>(std::min<int64_t>(part, EV_MAX_PART));
   const uint32_t smem = static_cast<uint32_t>(sizeof(EvictSmem)) + static_cast<uint32_t>(p.part_cap) * 4u;
-  const dim3 grid(EV_CTAS, static_cast<unsigned>(cache->Hkv), static_cast<unsigned>(cache->n_seqs));
   const Range range("hs2 cache_evict");
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (kv8) {
-    if (int rc = set_smem(cache_evict_kernel<true>, smem)) return rc;
-    cache_evict_kernel<true><<<grid, EV_THREADS, smem, st>>>(p);
-  } else {
-    if (int rc = set_smem(cache_evict_kernel<false>, smem)) return rc;
-    cache_evict_kernel<false><<<grid, EV_THREADS, smem, st>>>(p);
-  }
-  return launched();
+  return kv8 ? launch_evict(cache_evict_kernel<true>, p, cache, ctas, smem, static_cast<cudaStream_t>(stream))
+             : launch_evict(cache_evict_kernel<false>, p, cache, ctas, smem, static_cast<cudaStream_t>(stream));
 }
 
 int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const void* v, const int32_t* cu_q,
@@ -332,7 +385,10 @@ int hs2_tree_attn(const hs2_cache* cache, const hs2_draft* draft, const void* q,
     return HS2_ERR_UNSUPPORTED;
   const TreePlan plan = tree_plan();
   if (workspace_bytes < plan.bytes) return HS2_ERR_WORKSPACE;
-  TreeParams p = tree_params(cache, draft);
+  // the smallest block of rows that holds a sequence's drafted tokens
+  const int most = draft->max_draft * (draft->Hq / cache->Hkv);
+  const int rb = most <= 32 ? 32 : most <= 64 ? 64 : 128;
+  TreeParams p = tree_params(cache, draft, rb);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.o_tok = draft->q_tok_stride;
   p.o_head = draft->q_head_stride;
@@ -348,18 +404,15 @@ int hs2_tree_attn(const hs2_cache* cache, const hs2_draft* draft, const void* q,
   if (int rc = make_pool_map(&mv, cache, cache->v)) return rc;
   const Range range("hs2 tree_attn");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(plan.ctas);
-  if (cache->kv_dtype == HS2_KV_E4M3) {
-    if (int rc = set_smem(tree_attn_kernel<true>, TreeSmem<true>::BYTES)) return rc;
-    tree_attn_kernel<true><<<grid, tr_threads(true), TreeSmem<true>::BYTES, st>>>(mq, mk, mv, p);
-  } else {
-    if (int rc = set_smem(tree_attn_kernel<false>, TreeSmem<false>::BYTES)) return rc;
-    tree_attn_kernel<false><<<grid, tr_threads(false), TreeSmem<false>::BYTES, st>>>(mq, mk, mv, p);
+  const bool kv8 = cache->kv_dtype == HS2_KV_E4M3;
+  switch (rb) {
+    case 32: return kv8 ? launch_tree<true, 32>(mq, mk, mv, p, plan.ctas, most, st)
+                        : launch_tree<false, 32>(mq, mk, mv, p, plan.ctas, most, st);
+    case 64: return kv8 ? launch_tree<true, 64>(mq, mk, mv, p, plan.ctas, most, st)
+                        : launch_tree<false, 64>(mq, mk, mv, p, plan.ctas, most, st);
+    default: return kv8 ? launch_tree<true, 128>(mq, mk, mv, p, plan.ctas, most, st)
+                        : launch_tree<false, 128>(mq, mk, mv, p, plan.ctas, most, st);
   }
-  if (int rc = launched()) return rc;
-  const int rows = std::min(p.R, draft->max_draft) * p.G;  // of a unit
-  tree_merge_kernel<<<dim3(grid, static_cast<unsigned>((rows + 3) / 4)), 128, 0, st>>>(p);
-  return launched();
 }
 
 int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void* q, const float* lse,
@@ -372,7 +425,7 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   if (!q || !lse || !acc) return HS2_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(acc) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return HS2_ERR_UNSUPPORTED;
   WeightParams p{};
-  p.t = tree_params(cache, draft);
+  p.t = tree_params(cache, draft, 128);
   p.lse = lse;
   p.counted = counted;
   p.acc = acc;

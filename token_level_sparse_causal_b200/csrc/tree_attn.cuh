@@ -21,7 +21,13 @@
 //            (own S, P, O in tensor memory, own warpgroup) that take turns on
 //            the tensor core as in flash.cuh; their O join in the epilogue,
 //            where each warpgroup writes half of the columns;
-//   e4m3     codes arrive by TMA in a raw ring; four warps turn them into bf16
+//   few rows a tile's 128 rows are 4 blocks of 32 (2 of 64) copies of the unit's
+//            rows where those fit, and block k keeps only its share of the
+//            tile's keys (the rest of its P is zero): all warps share one row's
+//            exponentials, instead of one warp taking all of them (about 2000
+//            cycles a tile, 4500 with an e4m3 cache's scales). Each block is a
+//            softmax of its own; the epilogue adds the blocks' O;
+//   e4m3     codes arrive by TMA in a raw ring; eight warps turn them into bf16
 //            (exact; unlike f16 it leaves Q and P their whole range), another
 //            fetches the scales; the K scale multiplies the scores, the V
 //            scale multiplies P before its rounding;
@@ -35,12 +41,12 @@
 
 namespace hs2 {
 
-constexpr int TR_ITEMS = 6;      // bf16: tiles of 32 KB in the ring
-constexpr int TR_ITEMS_KV8 = 3;  // e4m3: converted tiles
-constexpr int TR_RAW = 5;        // e4m3: raw tiles of 16 KB
-constexpr int TR_SCALES = 4;     // e4m3: key tiles whose scales are held
+constexpr int TR_MAX_ITEMS = 6;  // tiles of 32 KB in the ring, at most
+constexpr int TR_MAX_RAW = 5;    // e4m3: raw tiles of 16 KB, at most
+constexpr int TR_SCALES = 8;     // e4m3: key tiles whose scales are held or on their way
 constexpr uint32_t RAW_BYTES = 128u * 128u;
-__host__ __device__ constexpr int tr_threads(bool kv8) { return kv8 ? 512 : 384; }
+constexpr int TR_CONV = 256;     // e4m3: converting threads
+__host__ __device__ constexpr int tr_threads(bool kv8) { return 384 + (kv8 ? TR_CONV : 0); }
 
 // What a call's kernels share: the unit geometry.
 struct TreeParams {
@@ -60,33 +66,37 @@ struct TreeParams {
 };
 
 struct TreeBars {
-  uint64_t full[TR_ITEMS], empty[TR_ITEMS];
-  uint64_t raw_full[TR_RAW], raw_empty[TR_RAW];
+  uint64_t full[TR_MAX_ITEMS], empty[TR_MAX_ITEMS];
+  uint64_t raw_full[TR_MAX_RAW], raw_empty[TR_MAX_RAW];
   uint64_t sc_full[TR_SCALES], sc_empty[TR_SCALES];
   uint64_t q_full, q_empty;
-  uint64_t v_raw[TR_ITEMS];  // a V tile landed whose rows behind the sequence are not yet zeroed
+  uint64_t v_raw[TR_MAX_ITEMS];  // a V tile landed whose rows behind the sequence are not yet zeroed
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t ml_ready, o_free;
+  uint64_t x_ready[2], x_free[2];  // the exchange of O between row blocks, per warpgroup
   uint64_t fin;
-  int64_t first;  // this CTA's stretch: first tile, number of tiles
-  int64_t count;
-  int64_t total;
+  int first, count;   // this CTA's stretch: first tile, number of tiles
   int b, unit, tile;  // where the stretch begins
-  int parts;          // CTAs that have work
+  int each, more;     // tiles of a CTA; the first `more` CTAs have one more
   uint32_t tmem_slot;
   int abort;
 };
 static_assert(sizeof(TreeBars) <= 512, "barrier area");
 
-template <bool KV8>
+// RB: rows of a block (32, 64 or 128); a unit has RB / G tokens.
+template <bool KV8, int RB>
 struct TreeSmem {
-  static constexpr int ITEMS = KV8 ? TR_ITEMS_KV8 : TR_ITEMS;
+  static constexpr int BLOCKS = 128 / RB;
+  static constexpr int ITEMS = KV8 ? 3 : BLOCKS > 1 ? 5 : 6;
+  static constexpr int RAWS = BLOCKS > 1 ? 4 : 5;
+  static_assert(ITEMS <= TR_MAX_ITEMS && RAWS <= TR_MAX_RAW, "rings");
   static constexpr uint32_t ITEM = TILE_BYTES;  // after Q
   static constexpr uint32_t RAW = ITEM + ITEMS * TILE_BYTES;
-  static constexpr uint32_t SCALE = RAW + (KV8 ? TR_RAW * RAW_BYTES : 0u);
+  static constexpr uint32_t SCALE = RAW + (KV8 ? RAWS * RAW_BYTES : 0u);
   static constexpr uint32_t BAR = SCALE + (KV8 ? TR_SCALES * 1024u : 0u);
-  static constexpr uint32_t ML = BAR + 512u;  // float2 [2][128]
-  static constexpr uint32_t BYTES = ML + 2048u;
+  static constexpr uint32_t ML = BAR + 512u;     // float2 [2][128]
+  static constexpr uint32_t EXCH = ML + 2048u;   // float [2][128 - RB][32]
+  static constexpr uint32_t BYTES = EXCH + 2u * (128 - RB) * 128u;
   static_assert(BYTES <= 232448u, "shared memory of one CTA");
 };
 
@@ -108,7 +118,7 @@ struct TreeWalk {
   int row0, T, ctx;     // its sequence
   int tiles, mtiles;    // key tiles of the unit, token tiles of the sequence
   int t0, t1;           // the segment's key tiles
-  int64_t left, pos;    // tiles left in the stretch, global index of t0
+  int left, pos;        // tiles left in the stretch, global index of t0
 
   __device__ __forceinline__ void load(const TreeParams& p) {
     tree_seq(p, b, row0, T, ctx);
@@ -124,7 +134,7 @@ struct TreeWalk {
     g = bars->unit / mtiles;
     m = bars->unit % mtiles;
     t0 = bars->tile;
-    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + left));
+    t1 = min(tiles, t0 + left);
     return true;
   }
   __device__ __forceinline__ bool next(const TreeParams& p) {
@@ -142,7 +152,7 @@ struct TreeWalk {
       }
     }
     t0 = 0;
-    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), left));
+    t1 = min(tiles, left);
     return true;
   }
   __device__ __forceinline__ int n() const { return t1 - t0; }
@@ -152,39 +162,46 @@ struct TreeWalk {
   __device__ __forceinline__ int last_rows() const { return t1 == tiles ? ctx + T - (tiles - 1) * 128 : 128; }
 };
 
-// One warp splits all tiles evenly and finds where this CTA's stretch begins.
-__device__ __forceinline__ void tree_split(const TreeParams& p, TreeBars* bars) {
+// A lane's share of a split: the key tiles of sequence b's units.
+__device__ __forceinline__ int64_t tree_cost(const TreeParams& p, int b, bool units, int where) {
+  if (b >= p.B) return 0;
+  int row0, T, ctx;
+  if (!tree_seq(p, b, row0, T, ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
+  return T ? static_cast<int64_t>((ctx + T + 127) >> 7) * p.Hkv * (units ? (T + p.R - 1) / p.R : 1) : 0;
+}
+
+// One warp splits all tiles evenly over the CTAs and finds where this CTA's
+// stretch begins.  units: sequences are counted once per token tile.
+template <typename Bars>
+__device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool units, int where) {
   const int lane = threadIdx.x & 31;
-  auto cost = [&](int b) -> int64_t {
-    if (b >= p.B) return 0;
-    int row0, T, ctx;
-    if (!tree_seq(p, b, row0, T, ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, 801);
-    return T ? static_cast<int64_t>((ctx + T + 127) >> 7) * p.Hkv * ((T + p.R - 1) / p.R) : 0;
-  };
-  int64_t total = 0;
-  for (int b = lane; b < p.B; b += 32) total += cost(b);
+  const int64_t mine = tree_cost(p, lane, units, where);  // the first 32 sequences, used twice
+  int64_t total64 = mine;
+  for (int b = lane + 32; b < p.B; b += 32) total64 += tree_cost(p, b, units, where);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  const int c = blockIdx.x;
-  int64_t first = 0, count = 0;
-  if (c < parts) {
-    first = c * total / parts;
-    count = (c + 1) * total / parts - first;
+  for (int o = 16; o > 0; o >>= 1) total64 += __shfl_xor_sync(0xffffffffu, total64, o);
+  if (total64 > 0x7fffffff) {  // beyond any cache; no part of it is done
+    if (lane == 0 && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
+    total64 = 0;
   }
+  const int total = static_cast<int>(total64);
+  const int each = total / static_cast<int>(gridDim.x), more = total - each * static_cast<int>(gridDim.x);
+  const int c = blockIdx.x;
+  const int first = c * each + min(c, more), count = each + (c < more ? 1 : 0);
   if (lane == 0) {
     bars->first = first;
     bars->count = count;
-    bars->total = total;
-    bars->parts = parts;
+    bars->each = each;
+    bars->more = more;
   }
   if (count == 0) return;
-  int64_t before = 0;
+  int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int64_t w = cost(b0 + lane), incl = w;
+    const int w = static_cast<int>(b0 == 0 ? mine : tree_cost(p, b0 + lane, units, where));
+    int incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
     const bool here = first >= before + incl - w && first < before + incl;
@@ -192,10 +209,10 @@ __device__ __forceinline__ void tree_split(const TreeParams& p, TreeBars* bars) 
       int row0, T, ctx;
       tree_seq(p, b0 + lane, row0, T, ctx);
       const int tiles = (ctx + T + 127) >> 7;
-      const int64_t rest = first - (before + incl - w);
+      const int rest = first - (before + incl - w);
       bars->b = b0 + lane;
-      bars->unit = static_cast<int>(rest / tiles);
-      bars->tile = static_cast<int>(rest % tiles);
+      bars->unit = rest / tiles;
+      bars->tile = rest % tiles;
     }
     if (__any_sync(0xffffffffu, here)) return;
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -243,15 +260,16 @@ __device__ __forceinline__ void tree_visible(int ctx, int base, uint64_t bits, u
   w[3] = static_cast<uint32_t>(hi >> 32);
 }
 
-// Sixteen e4m3 codes -> sixteen bf16 values (exact, NaN stays NaN).
+// Sixteen e4m3 codes -> sixteen bf16 values (exact, NaN stays NaN).  The
+// conversion instructions beat shifting the bits into place (525 against 673
+// cycles a tile of 128 x 128 by 128 threads).
 __device__ __forceinline__ void e4m3x16_to_bf16(uint4 raw, uint4& a, uint4& b) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   uint32_t f[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const uint32_t h = e4m3x2_to_f16x2(w[q >> 1] >> (16 * (q & 1)));
-    const __half2 h2 = *reinterpret_cast<const __half2*>(&h);
-    const float2 v = __half22float2(h2);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
     f[q] = pack_bf16x2(v.x, v.y);
   }
   a = make_uint4(f[0], f[1], f[2], f[3]);
@@ -259,31 +277,37 @@ __device__ __forceinline__ void e4m3x16_to_bf16(uint4 raw, uint4& a, uint4& b) {
 }
 
 // A raw tile of 128 rows of codes -> a bf16 tile in two 128-byte-swizzled
-// halves, by 128 threads (pt); rows from `keys` on become zeros.
+// halves, by TR_CONV threads (pt); rows from `keys` on become zeros.  No
+// branch, so that a thread's rows overlap.
 __device__ __forceinline__ void convert_tile(uint32_t raw_tile, uint32_t tile, int keys, int pt) {
+  constexpr int STEP = TR_CONV / 8, ROWS = 128 / STEP;
   const int c8 = pt & 7, row0 = pt >> 3;
-  uint4 raw[8];
+  // lanes 0-3 and 4-7 of a row store their two chunks in opposite order, so
+  // that a store touches every bank once
+  const bool flip = c8 >= 4;
+  const uint32_t src = raw_tile + row0 * 128 + c8 * 16;
+  // a step keeps row & 7, so the chunks' places only move by whole rows
+  const uint32_t dst1 = tile + sw128_chunk_offset(row0, 2 * c8 + (flip ? 1 : 0), 128);
+  const uint32_t dst2 = tile + sw128_chunk_offset(row0, 2 * c8 + (flip ? 0 : 1), 128);
+  uint4 raw[ROWS];
 #pragma unroll
-  for (int it = 0; it < 8; ++it) raw[it] = ld_shared_v4(raw_tile + (row0 + 16 * it) * 128 + c8 * 16);
+  for (int it = 0; it < ROWS; ++it) raw[it] = ld_shared_v4(src + it * STEP * 128);
 #pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    const int row = row0 + 16 * it;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (row < keys) e4m3x16_to_bf16(raw[it], a, b);
-    // lanes 0-3 and 4-7 of a row store their two chunks in opposite order, so
-    // that a store touches every bank once
-    const bool flip = c8 >= 4;
-    st_shared_v4(tile + sw128_chunk_offset(row, 2 * c8 + (flip ? 1 : 0), 128), flip ? b : a);
-    st_shared_v4(tile + sw128_chunk_offset(row, 2 * c8 + (flip ? 0 : 1), 128), flip ? a : b);
+  for (int it = 0; it < ROWS; ++it) {
+    if (row0 + STEP * it >= keys) raw[it] = make_uint4(0, 0, 0, 0);
+    uint4 a, b;
+    e4m3x16_to_bf16(raw[it], a, b);
+    st_shared_v4(dst1 + it * STEP * 128, flip ? b : a);
+    st_shared_v4(dst2 + it * STEP * 128, flip ? a : b);
   }
 }
 
-template <bool KV8>
+template <bool KV8, int RB>
 __global__ void __launch_bounds__(tr_threads(KV8), 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const TreeParams p) {
-  using SM = TreeSmem<KV8>;
-  constexpr int ITEMS = SM::ITEMS;
+  using SM = TreeSmem<KV8, RB>;
+  constexpr int ITEMS = SM::ITEMS, RAWS = SM::RAWS, BLOCKS = SM::BLOCKS;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   uint8_t* smem = tree_smem;
   TreeBars* bars = reinterpret_cast<TreeBars*>(smem + SM::BAR);
@@ -291,8 +315,11 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
   float* scales = reinterpret_cast<float*>(smem + SM::SCALE);  // [slot][K, V][128]
   const uint32_t q_base = smem_u32(smem);
   const uint32_t item_base = smem_u32(smem + SM::ITEM);
+  const uint32_t exch_base = smem_u32(smem + SM::EXCH);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort;
+  // tree_merge_kernel may be set up meanwhile; it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (q_base & 1023u) {  // the swizzled tiles need it; the whole CTA leaves
     if (threadIdx.x == 0) {
       p.part_unit[blockIdx.x] = make_int4(0, 0, 0, -1);
@@ -303,14 +330,14 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ITEMS; ++s) {
-      mbar_init(&bars->full[s], KV8 ? 128u : 1u);
+      mbar_init(&bars->full[s], KV8 ? TR_CONV / 32 : 1);
       mbar_init(&bars->empty[s], 1);
       mbar_init(&bars->v_raw[s], 1);
     }
     if (KV8) {
-      for (int s = 0; s < TR_RAW; ++s) {
+      for (int s = 0; s < RAWS; ++s) {
         mbar_init(&bars->raw_full[s], 1);
-        mbar_init(&bars->raw_empty[s], 128);
+        mbar_init(&bars->raw_empty[s], TR_CONV / 32);
       }
       for (int s = 0; s < TR_SCALES; ++s) {
         mbar_init(&bars->sc_full[s], 32);
@@ -323,6 +350,10 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->p_ready[x], 4);
       mbar_init(&bars->o_done[x], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->x_ready[x], RB < 128 ? 4 - RB / 32 : 1);
+      mbar_init(&bars->x_free[x], RB / 32);
     }
     mbar_init(&bars->ml_ready, 8);
     mbar_init(&bars->o_free, 8);
@@ -337,32 +368,35 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     tmem_alloc(&bars->tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp == 2) tree_split(p, bars);
+  if (warp == 2) tree_split(p, bars, true, 801);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
   // Registers move to the two softmax warpgroups (a row of scores is 128 of
-  // them); the shares of all warpgroups add up to what the CTA was launched
-  // with: 3 x 168 = 2 x 208 + 88, with an e4m3 cache 4 x 128 = 2 x 184 + 2 x 72.
+  // them); the shares of all warpgroups add up to no more than the CTA was
+  // launched with: 2 x 208 + 88 = 3 x 168; with an e4m3 cache (640 threads of
+  // 96, the scores read in quarters) 2 x 128 + 3 x 72 <= 5 x 96.
   if (warp >= 4 && warp < 12) {
-    reg_acquire<KV8 ? 184 : 208>();
+    reg_acquire<KV8 ? 128 : 208>();
     // ============================================ softmax / rescale / epilogue
     const int x = (warp >= 8) ? 1 : 0;
     const int r = threadIdx.x - 128 - 128 * x;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + x * 128;
     const uint32_t o_tm = tmem + lane_off + 256;  // O of x at + 128 x
-    const int tok_r = r / p.G, head_r = r % p.G;
-    int ns = 0, no1 = 0, seg = 0, ti = 0;  // waits taken on s_full[x] and o_done[1]; segments; tiles
+    const int block = r / RB, row_r = r % RB;  // this thread's keys of a tile, its query row
+    const int tok_r = row_r / p.G, head_r = row_r % p.G;
+    // waits taken on s_full[x] and o_done[1]; segments; tiles; exchanges
+    int ns = 0, no1 = 0, seg = 0, ti = 0, ex = 0;
     TreeWalk w;
     bool ok = w.begin(p, bars);
     if (threadIdx.x == 128) p.part_unit[blockIdx.x] = make_int4(0, 0, 0, -1);  // also if a wait runs out below
     while (ok) {
       const int n = w.n();
       const int t = w.m * p.R + tok_r;
-      const bool row_live = r < p.R * p.G && t < w.T;
-      const bool warp_live = (warp & 3) * 32 < w.rows(p);
+      const bool row_live = row_r < p.R * p.G && t < w.T;
+      const bool warp_live = (warp & 3) * 32 % RB < w.rows(p);
       uint64_t bits = 0;
       if (row_live) {
         bits = p.mask ? p.mask[w.row0 + t] : (2ull << t) - 1;  // t = 63: 2 << 63 = 0, minus 1: all
@@ -379,32 +413,25 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           sc_s = scales + slot * 256;
         }
         if (warp_live) {
-          uint32_t sr[4][32];
-          load_scores(s_tm, sr);
-          if (KV8) {
-            const uint64_t* ks2 = reinterpret_cast<const uint64_t*>(sc_s);
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              float a0, a1;
-              f2_unpack(f2_mul(f2_pack(__uint_as_float(sr[c >> 4][2 * (c & 15)]),
-                                       __uint_as_float(sr[c >> 4][2 * (c & 15) + 1])),
-                               ks2[c]),
-                        a0, a1);
-              sr[c >> 4][2 * (c & 15)] = __float_as_uint(a0);
-              sr[c >> 4][2 * (c & 15) + 1] = __float_as_uint(a1);
-            }
-          }
           const int base = (w.t0 + j) * 128;
-          if (base + 128 > w.ctx) {
-            uint32_t vis[4];
-            tree_visible(w.ctx, base, bits, vis);
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (!(vis[c >> 5] >> (c & 31) & 1u)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-          }
+          const bool edge = base + 128 > w.ctx;
+          uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+          if (edge) tree_visible(w.ctx, base, bits, vis);
           float alpha;
-          const bool resc =
-              softmax_tile<KV8>(s_tm, sr, KV8 ? 1.f : p.scale_log2, KV8 ? sc_s + 128 : nullptr, st, alpha);
+          bool resc;
+          if constexpr (KV8 || BLOCKS > 1) {
+            resc = softmax_quarters<RB / 32, KV8>(s_tm, block * (RB / 32), p.scale_log2, sc_s, sc_s + 128, edge, vis,
+                                                  st, alpha);
+          } else {
+            uint32_t sr[4][32];
+            load_scores(s_tm, sr);
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (!(vis[c >> 5] >> (c & 31) & 1u)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            }
+            resc = softmax_tile(s_tm, sr, p.scale_log2, st, alpha);
+          }
           // P V(j - 2) completed before S(j): s_full's commit covers it
           if (j >= 2 && __any_sync(0xffffffffu, resc)) rescale_row(o_tm + 128 * x, alpha);
           tmem_st_wait();
@@ -417,9 +444,9 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         }
       }
       if (!ok) break;
-      // ---- epilogue: join the even and the odd tiles' O.  Once O is done the
-      // (m, l) area is free: this segment's products waited (o_free) for every
-      // warp to be through with the last segment's.
+      // ---- epilogue: join the O of the even and the odd tiles and of the row
+      // blocks.  Once O is done the (m, l) area is free: this segment's products
+      // waited (o_free) for every warp to be through with the last segment's.
       ok = warp_wait(&bars->o_done[0], seg & 1, p.limit_ns, abort_flag, 843);
       if (ok && n > 1) ok = warp_wait(&bars->o_done[1], no1++ & 1, p.limit_ns, abort_flag, 845);
       if (!ok) break;
@@ -428,51 +455,100 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       if (lane == 0) mbar_arrive(&bars->ml_ready);
       if (!(ok = warp_wait(&bars->ml_ready, seg & 1, p.limit_ns, abort_flag, 844))) break;
       tc_fence_after();
-      if (warp_live) {
-        const float2 a = ml[r], c2 = ml[128 + r];
-        const float M = fmaxf(a.x, c2.x);
-        const float wa = (a.x == -INFINITY) ? 0.f : ex2_approx(a.x - M);
-        const float wb = (c2.x == -INFINITY) ? 0.f : ex2_approx(c2.x - M);
-        const float L = a.y * wa + c2.y * wb;
-        const bool whole = w.whole();
-        const float inv = !whole ? 1.f : (L > 0.f ? 1.f / L : 0.f);
-        const int64_t row = w.row0 + t;
-        const int h = w.g * p.G + head_r;
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 == 0 ? 1 : 0);
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * BLOCKS; ++k) M = fmaxf(M, ml[k * RB + row_r].x);
+#pragma unroll
+      for (int k = 0; k < 2 * BLOCKS; ++k) {
+        const float2 q = ml[k * RB + row_r];
+        L += q.x == -INFINITY ? q.y : q.y * ex2_approx(q.x - M);  // without a max: 0, or the NaN of its scores
+      }
+      const float ma = ml[r].x, mb = ml[128 + r].x;
+      const float wa = ma == -INFINITY ? 0.f : ex2_approx(ma - M);
+      const float wb = mb == -INFINITY ? 0.f : ex2_approx(mb - M);
+      const bool whole = w.whole();
+      const float inv = !whole ? 1.f : (L == 0.f ? 0.f : 1.f / L);
+      const int64_t row = w.row0 + t;
+      const int h = w.g * p.G + head_r;
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 == 0 ? 1 : 0);
 #pragma unroll 1
-        for (int c = 2 * x; c < 2 * x + 2; ++c) {  // this warpgroup's half of the columns
+      for (int c = 2 * x; c < 2 * x + 2; ++c) {  // this warpgroup's half of the columns
+        float v[32];
+        if (warp_live) {
           uint32_t oa[32], ob[32];
           tmem_ld32(o_tm + c * 32, oa);
           if (n > 1) tmem_ld32(o_tm + 128 + c * 32, ob);
           tmem_ld_wait();
           reg_fence(oa);
           if (n > 1) reg_fence(ob);
-          float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             // an O without a visible key holds nothing to add, whatever is there
             float y = wa > 0.f ? __uint_as_float(oa[e]) * wa : 0.f;
             if (n > 1 && wb > 0.f) y = fmaf(__uint_as_float(ob[e]), wb, y);
-            v[e] = y * inv;
-          }
-          if (row_live && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + c * 32);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                  pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-          } else if (row_live) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * 128 + r) * 128 + c * 32);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            v[e] = y;
           }
         }
-        if (row_live && x == 0) {
-          if (!whole)
-            p.part_ml[slot * 128 + r] = make_float2(M, L);
-          else if (p.lse)
-            p.lse[static_cast<int64_t>(h) * p.n_tok + row] = (M + log2f(L)) * 0.69314718055994530942f;
+        if (BLOCKS > 1) {
+          // the other blocks hand their part of the row to block 0 (16-byte
+          // chunks at a place XOR-ed with the row, so that eight lanes hit
+          // eight bank groups)
+          const uint32_t area = exch_base + static_cast<uint32_t>(x * (128 - RB)) * 128u;
+          if (block > 0) {
+            if (ex > 0 && !(ok = warp_wait(&bars->x_free[x], (ex - 1) & 1, p.limit_ns, abort_flag, 846))) break;
+            if (warp_live) {
+              const uint32_t at = area + static_cast<uint32_t>(r - RB) * 128u;
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                st_shared_v4(at + ((q ^ (r & 7)) << 4),
+                             make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->x_ready[x]);
+            ++ex;
+            continue;
+          }
+          if (!(ok = warp_wait(&bars->x_ready[x], ex & 1, p.limit_ns, abort_flag, 847))) break;
+          if (warp_live) {
+#pragma unroll
+            for (int k = 1; k < BLOCKS; ++k) {
+              const uint32_t at = area + static_cast<uint32_t>((k - 1) * RB + row_r) * 128u;
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const uint4 y = ld_shared_v4(at + ((q ^ (row_r & 7)) << 4));
+                v[4 * q] += __uint_as_float(y.x);
+                v[4 * q + 1] += __uint_as_float(y.y);
+                v[4 * q + 2] += __uint_as_float(y.z);
+                v[4 * q + 3] += __uint_as_float(y.w);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->x_free[x]);
+          ++ex;
         }
+        if (!warp_live || !row_live) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + c * 32);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= inv;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * 128 + row_r) * 128 + c * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+      }
+      if (!ok) break;
+      if (row_live && x == 0 && block == 0) {
+        if (!whole)
+          p.part_ml[slot * 128 + row_r] = make_float2(M, L);
+        else if (p.lse)
+          p.lse[static_cast<int64_t>(h) * p.n_tok + row] = (M + log2f(L)) * 0.69314718055994530942f;
       }
       tc_fence_before();
       __syncwarp();
@@ -482,9 +558,10 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       // the stretch's last segment may be a unit's first part
       if (threadIdx.x == 128 && w.left == n) {
         const bool head = w.t0 == 0 && w.t1 < w.tiles;
-        const int64_t end = w.pos + w.tiles;  // of the unit (its segment begins at tile 0)
-        p.part_unit[blockIdx.x] =
-            make_int4(w.b, w.g, w.m, head ? static_cast<int>((end * bars->parts - 1) / bars->total) : -1);
+        // the CTA with the unit's last tile (its segment begins at tile 0)
+        const int end = w.pos + w.tiles - 1, big = bars->more * (bars->each + 1);
+        const int last = end < big ? end / (bars->each + 1) : bars->more + (end - big) / bars->each;
+        p.part_unit[blockIdx.x] = make_int4(w.b, w.g, w.m, head ? last : -1);
       }
       if (!w.next(p)) break;
     }
@@ -494,7 +571,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       // =========================================================== TMA loads
       TreeWalk w;
       const bool work = !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars);
-      constexpr int RING = KV8 ? TR_RAW : TR_ITEMS;
+      constexpr int RING = KV8 ? RAWS : ITEMS;
       constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
       uint64_t* full = KV8 ? bars->raw_full : bars->full;
       uint64_t* empty = KV8 ? bars->raw_empty : bars->empty;
@@ -601,16 +678,23 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           }
           for (int j = 0; j < n; ++j) {
             const int x = j & 1;
-            // V(j) and K(j + 2) normally landed long ago: nothing but P stands
-            // between its arrival and the products
-            ok = wait_item(item) && (j + 2 >= n || wait_item(item + 1));
+            // a bf16 V(j) and K(j + 2) normally landed long ago: nothing but P
+            // stands between its arrival and the products.  Of an e4m3 cache
+            // K(j + 2) may still be converted, so P V does not wait for it.
+            ok = wait_item(item) && (KV8 || j + 2 >= n || wait_item(item + 1));
             // the last segment's O has been read
             if (ok && j == 0 && seg > 0) ok = mbar_wait(&bars->o_free, (seg - 1) & 1, p.limit_ns, abort_flag, 824);
             if (ok) ok = mbar_wait(&bars->p_ready[x], np[x]++ & 1, p.limit_ns, abort_flag, 825);
             if (!ok) break;
             tc_fence_after();
             issue_pv(x, item++, j < 2, j + 2 >= n);
-            if (j + 2 < n) issue_s(x, item++, j + 3 == n);
+            if (j + 2 < n) {
+              if (KV8) {
+                if (!(ok = wait_item(item))) break;
+                tc_fence_after();
+              }
+              issue_s(x, item++, j + 3 == n);
+            }
           }
           ++seg;
           if (!ok || !w.next(p)) break;
@@ -627,9 +711,12 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         int seg = 0;
         do {
           if (seg > 0 && !mbar_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 816)) break;
-          mbar_arrive_expect_tx(&bars->q_full, 2 * half);
-          tma_load_3d(smem, &tmQ, &bars->q_full, 0, w.g * p.G, w.row0 + w.m * p.R);
-          tma_load_3d(smem + HALF_BYTES, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
+          mbar_arrive_expect_tx(&bars->q_full, 2 * BLOCKS * half);
+          for (int k = 0; k < BLOCKS; ++k) {  // the same rows for every block
+            uint8_t* dst = smem + k * RB * 128;
+            tma_load_3d(dst, &tmQ, &bars->q_full, 0, w.g * p.G, w.row0 + w.m * p.R);
+            tma_load_3d(dst + HALF_BYTES, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
+          }
           ++seg;
         } while (w.next(p));
         wait_done(&bars->q_full, (seg - 1) & 1, p.limit_ns, 815);
@@ -654,41 +741,43 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
             }
           } while (w.next(p));
         } else {
-          // ================================================ scales of the keys
+          // ============ scales of the keys: asynchronous copies, several tiles ahead
           int ti = 0;
           bool ok = true;
           do {
             const int len = w.ctx + w.T;
             const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
-            for (int t = w.t0; t < w.t1 && ok; ++t, ++ti) {
-              float ks[4], vs[4];
+            int pg[4];  // pages of this lane's keys, read one tile ahead
+            auto pages_of = [&](int t) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int at = t * 128 + lane + 32 * e;
-                ks[e] = vs[e] = 0.f;
-                if (at < len) {
-                  const int pg = table[at >> p.page_log2];
-                  if (pg >= 0 && pg < p.n_pages) {
-                    const int64_t tok = (static_cast<int64_t>(pg) << p.page_log2) + (at & ((1 << p.page_log2) - 1));
-                    ks[e] = p.ksc[tok * p.Hkv + w.g] * p.scale_log2;
-                    vs[e] = p.vsc[tok * p.Hkv + w.g];
-                  }
-                }
+                pg[e] = (t < w.t1 && at < len) ? table[at >> p.page_log2] : -1;
               }
+            };
+            pages_of(w.t0);
+            for (int t = w.t0; t < w.t1; ++t, ++ti) {
               const int slot = ti % TR_SCALES;
-              if (ti >= TR_SCALES &&
-                  !mbar_wait(&bars->sc_empty[slot], ((ti / TR_SCALES) - 1) & 1, p.limit_ns, abort_flag, 832)) {
+              if (ti >= TR_SCALES && !warp_wait(&bars->sc_empty[slot], ((ti / TR_SCALES) - 1) & 1, p.limit_ns,
+                                                abort_flag, 832)) {
                 ok = false;
                 break;
               }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                scales[slot * 256 + lane + 32 * e] = ks[e];
-                scales[slot * 256 + 128 + lane + 32 * e] = vs[e];
+                const int at = t * 128 + lane + 32 * e;
+                const bool have = pg[e] >= 0 && pg[e] < p.n_pages;  // a page outside the pools reads as zeros
+                const int64_t tok =
+                    have ? (static_cast<int64_t>(pg[e]) << p.page_log2) + (at & ((1 << p.page_log2) - 1)) : 0;
+                const uint32_t dst = smem_u32(scales + slot * 256 + lane + 32 * e);
+                cp_async_4(dst, p.ksc + tok * p.Hkv + w.g, have ? 4u : 0u);
+                cp_async_4(dst + 512, p.vsc + tok * p.Hkv + w.g, have ? 4u : 0u);
               }
-              mbar_arrive(&bars->sc_full[slot]);
+              cp_async_arrive(&bars->sc_full[slot]);
+              pages_of(t + 1);
             }
           } while (ok && w.next(p));
+          cp_async_wait_all();  // nothing may be on its way into memory the CTA gives back
         }
       }
     } else {
@@ -706,14 +795,17 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
             bool is_v;
             tree_item(u, n, tile, is_v);
             const int keys = len - (w.t0 + tile) * 128;  // rows from here on are behind the sequence
-            const int rs = item % TR_RAW, cs = item % ITEMS;
-            ok = mbar_wait(&bars->raw_full[rs], (item / TR_RAW) & 1, p.limit_ns, abort_flag, 851) &&
-                 (item < ITEMS || mbar_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 852));
+            const int rs = item % RAWS, cs = item % ITEMS;
+            ok = warp_wait(&bars->raw_full[rs], (item / RAWS) & 1, p.limit_ns, abort_flag, 851) &&
+                 (item < ITEMS || warp_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 852));
             if (!ok) break;
             convert_tile(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, keys, pt);
             fence_proxy_async_smem();
-            mbar_arrive(&bars->full[cs]);
-            mbar_arrive(&bars->raw_empty[rs]);
+            __syncwarp();  // one arrival per warp: 256 of them would take longer than the conversion
+            if (lane == 0) {
+              mbar_arrive(&bars->full[cs]);
+              mbar_arrive(&bars->raw_empty[rs]);
+            }
           }
         } while (ok && w.next(p));
       }
@@ -732,6 +824,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
 // Joins the parts of the units that several CTAs share: block (c, y) takes rows
 // 4y .. 4y + 3 (one warp each) of the unit whose first part CTA c holds.
 __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched beside tree_attn_kernel's end
   const int c = blockIdx.x;
   const int4 u = p.part_unit[c];
   if (u.w < 0) return;
@@ -760,7 +853,7 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
     acc.z = fmaf(v.z, wt, acc.z);
     acc.w = fmaf(v.w, wt, acc.w);
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   const int h = u.y * p.G + r % p.G;
   const int64_t row = row0 + t;
   *reinterpret_cast<uint2*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + lane * 4) =

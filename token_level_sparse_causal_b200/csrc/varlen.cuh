@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
       load_scores(s_tm, sr);
       if (j * 128 + 127 > first + off) mask_after(sr, limit - j * 128);
       float alpha;
-      const bool resc = softmax_tile<false>(s_tm, sr, p.scale_log2, nullptr, st, alpha);
+      const bool resc = softmax_tile(s_tm, sr, p.scale_log2, st, alpha);
       // P V(j - 1) completed before S(j): s_full's commit covers it
       if (j > 0 && __any_sync(0xffffffffu, resc)) rescale_row(o_tm, alpha);
       tmem_st_wait();
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
     const bool row_live = (x == 0 || has_b) && r < R * p.G && i_row < nq;
     if (ok && (nX == 0 || warp_wait(&bars->o_done[x], 0, p.limit_ns, abort_flag, 742))) {
       tc_fence_after();
-      const float inv = (st.l > 0.f) ? 1.f / st.l : 0.f;
+      const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
       __nv_bfloat16* orow =
           p.o + static_cast<int64_t>(q0 + i_row) * p.o_tok + static_cast<int64_t>(h) * p.o_head;
 #pragma unroll 1

@@ -282,8 +282,18 @@ def hs2_exp2_check(x, y_mufu, y_fma3, y_fma4, stream=None) -> None:
 
 # --------------------------------------------- serving around a paged cache --
 
-def _need(t: Optional[torch.Tensor], dtype, shape, what: str, contiguous: bool = True, like=None) -> None:
-    """Argument check of a device tensor; shape entries of None are free."""
+def _need(t: Optional[torch.Tensor], dtype, shape, what: str, contiguous: bool = True, device: int = None) -> None:
+    """Argument check of a device tensor (None passes); `device` is a CUDA device index.  One cheap pass when all is
+    well: a decode step makes a dozen of these."""
+    if t is None:
+        return
+    if (t.dtype is not dtype or t.shape != shape or (device is not None and t.get_device() != device)
+            or not (t.is_contiguous() if contiguous else t.stride(-1) == 1 or t.shape[-1] == 1)):
+        _need_slow(t, dtype, shape, what, contiguous, device)
+
+
+def _need_slow(t, dtype, shape, what, contiguous=True, device=None) -> None:
+    """_need with alternatives: a tuple of dtypes, and None for a free entry of the shape."""
     if t is None:
         return
     ok = t.dtype in (dtype if isinstance(dtype, tuple) else (dtype,)) and t.dim() == len(shape)
@@ -293,29 +303,37 @@ def _need(t: Optional[torch.Tensor], dtype, shape, what: str, contiguous: bool =
         raise ValueError(f"{what}: must be contiguous")
     if not contiguous and t.shape[-1] != 1 and t.stride(-1) != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{what}: on {t.device}, expected {like.device}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{what}: on {t.device}, expected device {device}")
 
 
 def _strides(t: torch.Tensor) -> tuple:
     """Token and head stride of a [tokens][H][d] tensor, with the packed value for a dimension of size 1 (whose
     stride torch leaves open)."""
-    n, H, d = t.shape
-    head = t.stride(1) if H > 1 else d
-    return (t.stride(0) if n > 1 else H * head), head
+    (n, H, d), s = t.shape, t.stride()
+    head = s[1] if H > 1 else d
+    return (s[0] if n > 1 else H * head), head
 
 
-def _call(name: str, device: torch.device, stream, *args) -> None:
-    """Call a library function whose last argument is the stream, on `device`
-    (its current stream unless one is given)."""
-    fn = getattr(lib(), name)
-    if device.type != "cuda":
-        raise ValueError(f"{name}: tensors must be on a CUDA device, got {device}")
-    if device.index != torch.cuda.current_device():
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name: str, device: int, stream, *args) -> None:
+    """Call a library function whose last argument is the stream, on CUDA device `device` (its current stream unless
+    one is given)."""
+    if device < 0:
+        raise ValueError(f"{name}: the tensors must be on a CUDA device")
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)), name)
+            return _call(name, device, stream, *args)
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(device)
     else:
-        _check(fn(*args, _stream(stream)), name)
+        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    rc = getattr(lib(), name)(*args, st)
+    if rc != HS2_OK:
+        raise Hs2Error(rc, name)
 
 
 def make_cache(k, v, page_table, page: int, k_scale=None, v_scale=None) -> Hs2Cache:
@@ -323,24 +341,24 @@ def make_cache(k, v, page_table, page: int, k_scale=None, v_scale=None) -> Hs2Ca
     float8_e4m3fn with fp32 scales [n_pages * page][Hkv]) and an int32 page
     table [n_seqs][max_pages] (None where only hs2_qk_norm_rope uses it)."""
     f8 = k.dtype in (torch.uint8, torch.float8_e4m3fn)
-    _need(k, (torch.uint8, torch.float8_e4m3fn) if f8 else torch.bfloat16, (None, None, 128), "k", contiguous=False)
-    _need(v, k.dtype, tuple(k.shape), "v", contiguous=False, like=k)
+    dev = k.get_device()
+    _need_slow(k, (torch.uint8, torch.float8_e4m3fn) if f8 else torch.bfloat16, (None, None, 128), "k", False)
+    _need(v, k.dtype, k.shape, "v", False, dev)
     if _strides(v) != _strides(k):
         raise ValueError("v: must have k's strides")
     if page <= 0 or k.shape[0] % page:
         raise ValueError(f"page: {page} does not divide the pools' {k.shape[0]} tokens")
     if f8 != (k_scale is not None) or f8 != (v_scale is not None):
         raise ValueError("k_scale, v_scale: given exactly with an e4m3 cache")
-    _need(k_scale, torch.float32, (k.shape[0], k.shape[1]), "k_scale", like=k)
-    _need(v_scale, torch.float32, (k.shape[0], k.shape[1]), "v_scale", like=k)
-    _need(page_table, torch.int32, (None, None), "page_table", like=k)
+    _need(k_scale, torch.float32, (k.shape[0], k.shape[1]), "k_scale", True, dev)
+    _need(v_scale, torch.float32, (k.shape[0], k.shape[1]), "v_scale", True, dev)
+    _need_slow(page_table, torch.int32, (None, None), "page_table", True, dev)
     n_seqs, max_pages = (0, 0) if page_table is None else page_table.shape
-    ptr = lambda t: None if t is None else t.data_ptr()
     c = Hs2Cache(Hkv=k.shape[1], d=k.shape[2], kv_dtype=HS2_KV_E4M3 if f8 else HS2_KV_BF16, page=page,
                  n_pages=k.shape[0] // page, n_seqs=n_seqs, max_pages=max_pages, tok_stride=_strides(k)[0],
-                 head_stride=_strides(k)[1], k=ptr(k), v=ptr(v), k_scale=ptr(k_scale), v_scale=ptr(v_scale),
-                 page_table=ptr(page_table))
-    c.tensors = (k, v, page_table, k_scale, v_scale)
+                 head_stride=_strides(k)[1], k=_addr(k), v=_addr(v), k_scale=_addr(k_scale), v_scale=_addr(v_scale),
+                 page_table=_addr(page_table))
+    c.tensors, c.device = (k, v, page_table, k_scale, v_scale), dev
     return c
 
 
@@ -349,69 +367,72 @@ def hs2_qk_norm_rope(cache: Hs2Cache, q, k, v, q_weight, k_weight, eps: float, i
     """q, q_out [n][Hq][128], k, v [n][Hkv][128] bf16 (any token and head strides), inv_freq float64 [rot / 2],
     positions and slots int32 [n] (slots None: rows 0 .. n - 1 of the pools; -1: no cache write)."""
     n, Hq, _ = q.shape
-    pool = cache.tensors[0]
-    _need(q, torch.bfloat16, (n, Hq, 128), "q", False, pool)
-    _need(q_out, torch.bfloat16, (n, Hq, 128), "q_out", False, pool)
-    _need(k, torch.bfloat16, (n, cache.Hkv, 128), "k", False, pool)
-    _need(v, torch.bfloat16, (n, cache.Hkv, 128), "v", False, pool)
-    if _strides(v) != _strides(k):
+    dev = cache.device
+    _need(q, torch.bfloat16, (n, Hq, 128), "q", False, dev)
+    _need(q_out, torch.bfloat16, (n, Hq, 128), "q_out", False, dev)
+    _need(k, torch.bfloat16, (n, cache.Hkv, 128), "k", False, dev)
+    _need(v, torch.bfloat16, (n, cache.Hkv, 128), "v", False, dev)
+    kv = _strides(k)
+    if _strides(v) != kv:
         raise ValueError("v: must have k's strides")
-    _need(q_weight, torch.bfloat16, (128,), "q_weight", True, pool)
-    _need(k_weight, torch.bfloat16, (128,), "k_weight", True, pool)
-    _need(inv_freq, torch.float64, (None,), "inv_freq", True, pool)
-    _need(positions, torch.int32, (n,), "positions", True, pool)
-    _need(slots, torch.int32, (n,), "slots", True, pool)
-    if slots is None and n > pool.shape[0]:
-        raise ValueError(f"slots: {n} rows do not fit the pools' {pool.shape[0]} tokens")
-    r = Hs2Rope(n, Hq, 2 * inv_freq.numel(), int(interleaved), eps, 0, *_strides(q), *_strides(k),
-                *_strides(q_out))
-    _call("hs2_qk_norm_rope", pool.device, stream, ctypes.byref(cache), ctypes.byref(r), _ptr(q), _ptr(k), _ptr(v),
-          _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(slots), _ptr(q_out))
+    _need(q_weight, torch.bfloat16, (128,), "q_weight", True, dev)
+    _need(k_weight, torch.bfloat16, (128,), "k_weight", True, dev)
+    _need(inv_freq, torch.float64, (inv_freq.numel(),), "inv_freq", True, dev)
+    _need(positions, torch.int32, (n,), "positions", True, dev)
+    _need(slots, torch.int32, (n,), "slots", True, dev)
+    if slots is None and n > cache.n_pages * cache.page:
+        raise ValueError(f"slots: {n} rows do not fit the pools' {cache.n_pages * cache.page} tokens")
+    r = Hs2Rope(n, Hq, 2 * inv_freq.numel(), int(interleaved), eps, 0, *_strides(q), *kv, *_strides(q_out))
+    _call("hs2_qk_norm_rope", dev, stream, ctypes.byref(cache), ctypes.byref(r), _addr(q), _addr(k), _addr(v),
+          _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), _addr(slots), _addr(q_out))
 
 
 def make_varlen(q, k, n_seqs: int) -> Hs2Varlen:
     """hs2_varlen for packed q [total_q][Hq][128] and k (v alike) [total_k][Hkv][128], bf16."""
-    _need(q, torch.bfloat16, (None, None, 128), "q", False)
-    _need(k, torch.bfloat16, (None, None, 128), "k", False, q)
+    _need_slow(q, torch.bfloat16, (None, None, 128), "q", False)
+    _need_slow(k, torch.bfloat16, (None, None, 128), "k", False, q.get_device())
     return Hs2Varlen(n_seqs, q.shape[0], k.shape[0], q.shape[1], k.shape[1], 128, *_strides(q), *_strides(k))
 
 
 def hs2_varlen_attn(shape: Hs2Varlen, q, k, v, cu_q, cu_k, o, lse=None, stream=None) -> None:
     """q, o [total_q][Hq][128], k, v [total_k][Hkv][128]; cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q);
     lse fp32 [Hq][total_q] or None.  q and o, and k and v, have the strides make_varlen saw."""
-    for t, n, h, st, name in ((q, shape.total_q, shape.Hq, (shape.q_tok_stride, shape.q_head_stride), "q"),
-                              (o, shape.total_q, shape.Hq, (shape.q_tok_stride, shape.q_head_stride), "o"),
-                              (k, shape.total_k, shape.Hkv, (shape.kv_tok_stride, shape.kv_head_stride), "k"),
-                              (v, shape.total_k, shape.Hkv, (shape.kv_tok_stride, shape.kv_head_stride), "v")):
-        _need(t, torch.bfloat16, (n, h, 128), name, False, q)
+    dev = q.get_device()
+    rows_q, st_q = (shape.total_q, shape.Hq, 128), (shape.q_tok_stride, shape.q_head_stride)
+    rows_k, st_k = (shape.total_k, shape.Hkv, 128), (shape.kv_tok_stride, shape.kv_head_stride)
+    for t, rows, st, name in ((q, rows_q, st_q, "q"), (o, rows_q, st_q, "o"), (k, rows_k, st_k, "k"),
+                              (v, rows_k, st_k, "v")):
+        _need(t, torch.bfloat16, rows, name, False, dev)
         if _strides(t) != st:
             raise ValueError(f"{name}: strides {_strides(t)}, expected {st}")
-    _need(cu_q, torch.int32, (shape.n_seqs + 1,), "cu_q", True, q)
-    _need(cu_k, torch.int32, (shape.n_seqs + 1,), "cu_k", True, q)
-    _need(lse, torch.float32, (shape.Hq, shape.total_q), "lse", True, q)
-    _call("hs2_varlen_attn", q.device, stream, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k),
-          _ptr(o), _ptr(lse))
+    _need(cu_q, torch.int32, (shape.n_seqs + 1,), "cu_q", True, dev)
+    _need(cu_k, torch.int32, (shape.n_seqs + 1,), "cu_k", True, dev)
+    _need(lse, torch.float32, (shape.Hq, shape.total_q), "lse", True, dev)
+    _call("hs2_varlen_attn", dev, stream, ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(cu_q), _addr(cu_k),
+          _addr(o), _addr(lse))
 
 
 def make_draft(q, cu_draft, ctx_len, mask, max_draft: int) -> Hs2Draft:
     """hs2_draft for queries shaped like q [n_tok][Hq][128]; cu_draft int32 [n_seqs + 1], ctx_len int32 [n_seqs],
     mask int64 or uint64 [n_tok] (None: chains)."""
-    _need(q, torch.bfloat16, (None, None, 128), "q", False)
-    _need(ctx_len, torch.int32, (None,), "ctx_len", True, q)
-    _need(cu_draft, torch.int32, (ctx_len.shape[0] + 1,), "cu_draft", True, q)
-    _need(mask, (torch.int64, torch.uint64), (q.shape[0],), "mask", True, q)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    d = Hs2Draft(q.shape[0], int(max_draft), q.shape[1], 0, *_strides(q), ptr(cu_draft), ptr(ctx_len), ptr(mask))
-    d.tensors = (cu_draft, ctx_len, mask)
+    dev = q.get_device()
+    _need_slow(q, torch.bfloat16, (None, None, 128), "q", False)
+    _need_slow(ctx_len, torch.int32, (None,), "ctx_len", True, dev)
+    _need(cu_draft, torch.int32, (ctx_len.shape[0] + 1,), "cu_draft", True, dev)
+    _need_slow(mask, (torch.int64, torch.uint64), (q.shape[0],), "mask", True, dev)
+    d = Hs2Draft(q.shape[0], int(max_draft), q.shape[1], 0, *_strides(q), _addr(cu_draft), _addr(ctx_len), _addr(mask))
+    d.tensors, d.n_seqs, d.device = (cu_draft, ctx_len, mask), ctx_len.shape[0], dev
     return d
 
 
 def _need_draft(cache: Hs2Cache, draft: Hs2Draft, q, o=None) -> None:
-    if draft.tensors[1].shape[0] != cache.n_seqs:
-        raise ValueError(f"draft: {draft.tensors[1].shape[0]} sequences, the cache has {cache.n_seqs}")
+    if draft.n_seqs != cache.n_seqs:
+        raise ValueError(f"draft: {draft.n_seqs} sequences, the cache has {cache.n_seqs}")
+    if draft.device != cache.device:
+        raise ValueError(f"draft: on device {draft.device}, the cache is on {cache.device}")
     for t, name in ((q, "q"), (o, "o")):
         if t is not None:
-            _need(t, torch.bfloat16, (draft.n_tok, draft.Hq, 128), name, False, cache.tensors[0])
+            _need(t, torch.bfloat16, (draft.n_tok, draft.Hq, 128), name, False, cache.device)
             if _strides(t) != (draft.q_tok_stride, draft.q_head_stride):
                 raise ValueError(f"{name}: strides {_strides(t)} are not the draft's")
 
@@ -426,33 +447,35 @@ def tree_attn_workspace_bytes(cache: Hs2Cache, draft: Hs2Draft) -> int:
 def hs2_tree_attn(cache: Hs2Cache, draft: Hs2Draft, q, o, lse, workspace, stream=None) -> None:
     """q, o [n_tok][Hq][128] bf16; lse fp32 [Hq][n_tok] or None; workspace of tree_attn_workspace_bytes."""
     _need_draft(cache, draft, q, o)
-    _need(lse, torch.float32, (draft.Hq, draft.n_tok), "lse", True, q)
-    _call("hs2_tree_attn", q.device, stream, ctypes.byref(cache), ctypes.byref(draft), _ptr(q), _ptr(o), _ptr(lse),
-          _ptr(workspace), workspace.numel() * workspace.element_size())
+    _need(lse, torch.float32, (draft.Hq, draft.n_tok), "lse", True, cache.device)
+    if workspace.get_device() != cache.device:
+        raise ValueError(f"workspace: on {workspace.device}, expected device {cache.device}")
+    _call("hs2_tree_attn", cache.device, stream, ctypes.byref(cache), ctypes.byref(draft), _addr(q), _addr(o),
+          _addr(lse), _addr(workspace), workspace.numel() * workspace.element_size())
 
 
 def hs2_cache_weights(cache: Hs2Cache, draft: Hs2Draft, q, lse, counted, acc, stream=None) -> None:
     """lse fp32 [Hq][n_tok] from hs2_tree_attn; counted uint8 [n_tok] or None; acc fp32 [n_seqs][Hkv][acc_stride]."""
     _need_draft(cache, draft, q)
-    _need(lse, torch.float32, (draft.Hq, draft.n_tok), "lse", True, q)
-    _need(counted, (torch.uint8, torch.bool), (draft.n_tok,), "counted", True, q)
-    _need(acc, torch.float32, (cache.n_seqs, cache.Hkv, None), "acc", True, q)
-    _call("hs2_cache_weights", q.device, stream, ctypes.byref(cache), ctypes.byref(draft), _ptr(q), _ptr(lse),
-          _ptr(counted), _ptr(acc), acc.shape[2])
+    _need(lse, torch.float32, (draft.Hq, draft.n_tok), "lse", True, cache.device)
+    _need_slow(counted, (torch.uint8, torch.bool), (draft.n_tok,), "counted", True, cache.device)
+    _need(acc, torch.float32, (cache.n_seqs, cache.Hkv, acc.shape[-1]), "acc", True, cache.device)
+    _call("hs2_cache_weights", cache.device, stream, ctypes.byref(cache), ctypes.byref(draft), _addr(q), _addr(lse),
+          _addr(counted), _addr(acc), acc.shape[2])
 
 
 def hs2_cache_evict(cache: Hs2Cache, seq_len, acc, keep: int, recent: int, idx, new_len, acc_out=None,
                     stream=None) -> None:
     """seq_len, new_len int32 [n_seqs]; acc (and acc_out, which may be acc) fp32 [n_seqs][Hkv][acc_stride];
     idx int32 [n_seqs][Hkv][keep]."""
-    pool, B = cache.tensors[0], cache.n_seqs
-    _need(seq_len, torch.int32, (B,), "seq_len", True, pool)
-    _need(new_len, torch.int32, (B,), "new_len", True, pool)
-    _need(acc, torch.float32, (B, cache.Hkv, None), "acc", True, pool)
-    _need(acc_out, torch.float32, tuple(acc.shape), "acc_out", True, pool)
-    _need(idx, torch.int32, (B, cache.Hkv, keep), "idx", True, pool)
-    _call("hs2_cache_evict", pool.device, stream, ctypes.byref(cache), _ptr(seq_len), _ptr(acc), _ptr(acc_out),
-          acc.shape[2], int(keep), int(recent), _ptr(idx), _ptr(new_len))
+    dev, B = cache.device, cache.n_seqs
+    _need(seq_len, torch.int32, (B,), "seq_len", True, dev)
+    _need(new_len, torch.int32, (B,), "new_len", True, dev)
+    _need(acc, torch.float32, (B, cache.Hkv, acc.shape[-1]), "acc", True, dev)
+    _need(acc_out, torch.float32, acc.shape, "acc_out", True, dev)
+    _need(idx, torch.int32, (B, cache.Hkv, keep), "idx", True, dev)
+    _call("hs2_cache_evict", dev, stream, ctypes.byref(cache), _addr(seq_len), _addr(acc), _addr(acc_out),
+          acc.shape[2], int(keep), int(recent), _addr(idx), _addr(new_len))
 
 
 # hs2_debug_set flag bits (include/hs2.h)
