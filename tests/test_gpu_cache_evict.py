@@ -105,8 +105,8 @@ def test_ties_signs_and_ranges(values, n, keep, recent):
 
 
 def test_rows_too_long_for_shared_memory():
-    """Above 16 x 40960 positions the keys are read from global memory in every pass."""
-    n = 16 * 40960 + 999
+    """Above 8 x 40960 positions the keys are read from global memory in every pass."""
+    n = 8 * 40960 + 999
     x = _case([n], 1, True, 128, seed=4, values="ties")
     d = _run(x, 5000, 128)
     hs2.hs2_sync()

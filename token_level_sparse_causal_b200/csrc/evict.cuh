@@ -28,14 +28,16 @@
 namespace hs2 {
 
 constexpr int EV_THREADS = 512;
-constexpr int EV_MAX_CTAS = 16;  // CTAs of a cluster
+constexpr int EV_MAX_CTAS = 8;  // CTAs of a cluster
 constexpr int EV_BINS = 2048;
+constexpr int EV_COARSE = 64;   // groups of 32 bins
 constexpr int EV_ROWS = 8;      // 16-byte pieces in flight per thread
 constexpr int EV_MAX_PART = 40960;  // keys a CTA holds in shared memory
+constexpr int EV_MAX_TABLE = 8192;  // page table entries held there
 static_assert(EV_THREADS == SEL_THREADS, "block_excl_scan");
 
 struct EvictParams {
-  int Hkv, page_log2, n_pages, max_pages, keep, recent, part_cap;
+  int Hkv, page_log2, n_pages, max_pages, keep, recent, part_cap, table_cap;
   uint8_t *k, *v;
   int64_t tok_b, head_b;  // bytes
   float *ksc, *vsc;
@@ -47,16 +49,55 @@ struct EvictParams {
 };
 
 struct EvictSmem {
-  uint32_t hist[3][EV_BINS];  // this CTA's counts of each pass, read by the other CTAs
+  uint32_t hist[3][EV_BINS];      // this CTA's counts of each pass, read by the other CTAs
+  uint32_t coarse[3][EV_COARSE];  // the same, 32 bins together
+  uint32_t part[EV_THREADS];
   uint32_t warp_gt[16], warp_eq[16];
   uint32_t cta_gt, cta_eq;    // read by the other CTAs
-  uint32_t scan[16];
   uint32_t sh[2];
-  uint32_t keys[];            // this CTA's part of the row
+  uint32_t keys[];  // this CTA's part of the row, then its page table
 };
 
+// Sums BINS counts over the cluster and finds the bin that holds rank k from the
+// top down: out = (bin, count in the bins above it).  BINS is 32 or 64.
+template <int BINS>
+__device__ __forceinline__ void ev_find(cooperative_groups::cluster_group& cl, uint32_t* counts, int ctas, uint32_t k,
+                                        uint32_t* part, uint32_t* out) {
+  static_assert(EV_THREADS / BINS >= EV_MAX_CTAS, "a thread reads one count");
+  const int tid = threadIdx.x, bin = tid % BINS, r = tid / BINS;
+  if (r < EV_MAX_CTAS) part[tid] = r < ctas ? cl.map_shared_rank(counts, r)[bin] : 0u;
+  __syncthreads();
+  if (tid < 32) {  // lane l: bins from the top down
+    constexpr int PER = BINS / 32;
+    uint32_t c[PER], sum = 0;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      c[q] = 0;
+#pragma unroll
+      for (int i = 0; i < EV_MAX_CTAS; ++i) c[q] += part[i * BINS + BINS - 1 - (PER * tid + q)];
+      sum += c[q];
+    }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (tid >= o) incl += y;
+    }
+    uint32_t run = incl - sum;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      if (run < k && run + c[q] >= k) {
+        out[0] = static_cast<uint32_t>(BINS - 1 - (PER * tid + q));
+        out[1] = run;
+      }
+      run += c[q];
+    }
+  }
+  __syncthreads();
+}
+
 template <bool KV8>
-__global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ __align__(16) uint8_t ev_raw[];
@@ -81,6 +122,17 @@ __global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictPara
     if (acc_out && acc_out != acc)
       for (int i = rank * EV_THREADS + tid; i < n; i += ctas * EV_THREADS) acc_out[i] = acc[i];
     return;
+  }
+
+  // the sequence's pages, where they fit
+  const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages;
+  {
+    const int pages = (n + (1 << p.page_log2) - 1) >> p.page_log2;
+    if (pages <= p.table_cap) {
+      int32_t* held_table = reinterpret_cast<int32_t*>(sm.keys + p.part_cap);
+      for (int i = tid; i < pages; i += EV_THREADS) held_table[i] = table[i];
+      table = held_table;  // read after the cluster's barriers below
+    }
   }
 
   // ---- select: the k-th largest key of the candidates
@@ -113,30 +165,25 @@ __global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictPara
         const uint32_t key = key_at(i);
         if ((key & pmask) == prefix) atomicAdd(&hist[(key >> shift) & dmask], 1u);
       }
-      cl.sync();  // each pass has counts of its own, so one barrier a pass is enough
-      // thread t owns four bins, from the top down (the last pass fills the lower half only)
-      const int bin0 = EV_BINS - 4 * (tid + 1);
-      uint32_t c[4] = {0, 0, 0, 0};
-      for (int r = 0; r < ctas; ++r) {
-        const uint4 x = reinterpret_cast<const uint4*>(cl.map_shared_rank(hist, r))[bin0 >> 2];
-        c[0] += x.x;
-        c[1] += x.y;
-        c[2] += x.z;
-        c[3] += x.w;
+      __syncthreads();
+      {  // groups of 32 bins: eight lanes add up four bins each
+        const uint4 x = reinterpret_cast<const uint4*>(hist)[tid];
+        uint32_t c = (x.x + x.y) + (x.z + x.w);
+        c += __shfl_xor_sync(0xffffffffu, c, 1);
+        c += __shfl_xor_sync(0xffffffffu, c, 2);
+        c += __shfl_xor_sync(0xffffffffu, c, 4);
+        if ((tid & 7) == 0) sm.coarse[pass][tid >> 3] = c;
       }
-      uint32_t tot;
-      const uint32_t loc = (c[0] + c[1]) + (c[2] + c[3]);
-      const uint32_t ex = block_excl_scan(loc, sm.scan, &tot);
-      if (ex < krem && ex + loc >= krem) {
-        uint32_t run = ex;
-#pragma unroll
-        for (int q = 3; q >= 0; --q) {
-          if (run < krem && run + c[q] >= krem) {
-            sm.sh[0] = static_cast<uint32_t>(bin0 + q);
-            sm.sh[1] = run;
-          }
-          run += c[q];
-        }
+      cl.sync();  // each pass has counts of its own, so one barrier a pass is enough
+      // the group that holds rank krem from the top, then the bin in it; both
+      // from the sums over the cluster, so that few words cross it
+      ev_find<EV_COARSE>(cl, sm.coarse[pass], ctas, krem, sm.part, sm.sh);
+      const uint32_t group = sm.sh[0], above = sm.sh[1];
+      __syncthreads();
+      ev_find<32>(cl, hist + 32 * group, ctas, krem - above, sm.part, sm.sh);
+      if (tid == 0) {
+        sm.sh[0] += 32 * group;
+        sm.sh[1] += above;
       }
       __syncthreads();
       prefix |= sm.sh[0] << shift;
@@ -171,15 +218,17 @@ __global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictPara
       sm.cta_eq = c;
     }
     cl.sync();
+    // counts before this warp's piece: lanes 0-15 the CTA's warps, 16 on the CTAs
     uint32_t gt_before = 0, eq_before = 0;
-    for (int r = 0; r < rank; ++r) {
-      gt_before += *cl.map_shared_rank(&sm.cta_gt, r);
-      eq_before += *cl.map_shared_rank(&sm.cta_eq, r);
+    if (lane < warp) {
+      gt_before = sm.warp_gt[lane];
+      eq_before = sm.warp_eq[lane];
+    } else if (lane >= 16 && lane - 16 < rank) {
+      gt_before = *cl.map_shared_rank(&sm.cta_gt, lane - 16);
+      eq_before = *cl.map_shared_rank(&sm.cta_eq, lane - 16);
     }
-    for (int w = 0; w < warp; ++w) {
-      gt_before += sm.warp_gt[w];
-      eq_before += sm.warp_eq[w];
-    }
+    gt_before = __reduce_add_sync(0xffffffffu, gt_before);
+    eq_before = __reduce_add_sync(0xffffffffu, eq_before);
     const uint32_t below = (1u << lane) - 1u;
     for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
       const int i = i0 + lane;
@@ -199,7 +248,6 @@ __global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictPara
 
   // ---- move: batches of rows, in ascending order, by the whole cluster
   constexpr int PIECES = KV8 ? 16 : 32;  // 16-byte pieces of a K row and a V row
-  const int32_t* table = p.table + static_cast<int64_t>(b) * p.max_pages;
   // token of the pools that holds position pos, or -1
   auto token_of = [&](int pos) -> int64_t {
     const int pg = table[pos >> p.page_log2];
@@ -215,27 +263,37 @@ __global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictPara
   const int row0 = rank * (EV_THREADS / PIECES) + tid / PIECES;
   const int batch = step * EV_ROWS;
   const int ctid = rank * EV_THREADS + tid;  // scalars of row ctid of a batch
-  for (int i0 = 0; i0 < p.keep; i0 += batch) {
-    uint4 data[EV_ROWS];
-    bool have[EV_ROWS];
+  int old[EV_ROWS];  // old positions of the batch's rows, read a batch ahead
+  auto olds_of = [&](int i0) {
 #pragma unroll
     for (int e = 0; e < EV_ROWS; ++e) {
       const int i = i0 + e * step + row0;
-      have[e] = false;
-      if (i < p.keep) {
-        const int64_t tok = token_of(idx[i]);
-        have[e] = tok >= 0;
-        if (have[e]) data[e] = *reinterpret_cast<const uint4*>(base + tok * p.tok_b);
+      old[e] = i < p.keep ? idx[i] : -1;
+    }
+  };
+  olds_of(0);
+  for (int i0 = 0; i0 < p.keep; i0 += batch) {
+    uint4 data[EV_ROWS];
+    uint32_t have = 0;
+#pragma unroll
+    for (int e = 0; e < EV_ROWS; ++e) {
+      if (old[e] >= 0) {
+        const int64_t tok = token_of(old[e]);
+        if (tok >= 0) {
+          data[e] = *reinterpret_cast<const uint4*>(base + tok * p.tok_b);
+          have |= 1u << e;
+        }
       }
     }
+    olds_of(i0 + batch);
     float x_acc = 0.f, x_ks = 0.f, x_vs = 0.f;
     int64_t from = -1;
     const int is = i0 + ctid;
     const bool scalar = ctid < batch && is < p.keep;
     if (scalar) {
-      const int old = idx[is];
-      x_acc = acc[old];
-      if (KV8 && (from = token_of(old)) >= 0) {
+      const int was = idx[is];
+      x_acc = acc[was];
+      if (KV8 && (from = token_of(was)) >= 0) {
         x_ks = p.ksc[from * p.Hkv + g];
         x_vs = p.vsc[from * p.Hkv + g];
       }
@@ -243,7 +301,7 @@ __global__ void __launch_bounds__(EV_THREADS) cache_evict_kernel(const EvictPara
     cl.sync();  // the batch is in registers
 #pragma unroll
     for (int e = 0; e < EV_ROWS; ++e) {
-      if (have[e]) {
+      if (have >> e & 1u) {
         const int64_t tok = token_of(i0 + e * step + row0);
         if (tok >= 0) *reinterpret_cast<uint4*>(base + tok * p.tok_b) = data[e];
       }

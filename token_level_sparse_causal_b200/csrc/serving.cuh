@@ -153,10 +153,6 @@ int launch_norm_rope(const NormRopeParams& p, bool kv8, bool pairs, cudaStream_t
 template <typename K>
 int launch_evict(K kernel, const EvictParams& p, const hs2_cache* c, int ctas, uint32_t smem, cudaStream_t st) {
   if (int rc = set_smem(kernel, smem)) return rc;
-  if (ctas > 8) {  // a cluster of 16 is allowed kernel by kernel
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-      return HS2_ERR_CUDA;
-  }
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = static_cast<unsigned>(ctas);
@@ -301,15 +297,17 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   p.acc_stride = acc_stride;
   p.idx = idx;
   p.new_len = new_len;
-  // CTAs a row: as many as keep every SM busy, up to the largest cluster
+  // CTAs a row: as many as run at once (two an SM), up to a portable cluster
+  // (clusters of 16 ran one a GPC and took longer)
   const int64_t rows = static_cast<int64_t>(cache->n_seqs) * cache->Hkv;
   int ctas = EV_MAX_CTAS;
-  while (ctas > 1 && rows * ctas > 4 * sm_count()) ctas /= 2;
-  // shared memory for the longest part a row of this cache can have
+  while (ctas > 1 && rows * ctas > 2 * sm_count()) ctas /= 2;
+  // shared memory for the longest part a row of this cache can have, and its pages
   const int64_t longest = std::min<int64_t>(acc_stride, static_cast<int64_t>(cache->max_pages) * cache->page);
   const int64_t part = ((longest + ctas - 1) / ctas + 3) & ~int64_t(3);
   p.part_cap = static_cast<int>(std::min<int64_t>(part, EV_MAX_PART));
-  const uint32_t smem = static_cast<uint32_t>(sizeof(EvictSmem)) + static_cast<uint32_t>(p.part_cap) * 4u;
+  p.table_cap = std::min(cache->max_pages, EV_MAX_TABLE);
+  const uint32_t smem = static_cast<uint32_t>(sizeof(EvictSmem)) + static_cast<uint32_t>(p.part_cap + p.table_cap) * 4u;
   const Range range("hs2 cache_evict");
   return kv8 ? launch_evict(cache_evict_kernel<true>, p, cache, ctas, smem, static_cast<cudaStream_t>(stream))
              : launch_evict(cache_evict_kernel<false>, p, cache, ctas, smem, static_cast<cudaStream_t>(stream));
