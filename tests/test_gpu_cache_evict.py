@@ -95,6 +95,16 @@ def test_matches_oracle(lens, Hkv, page, keep, recent, kv8):
     _check(x, d, keep, recent)
 
 
+@pytest.mark.parametrize("kv8", [False, True])
+def test_more_rows_than_sms(kv8):
+    """Above one row an SM a CTA has fewer threads: 160 rows, every length from none to some hundreds."""
+    rng = np.random.default_rng(8)
+    x = _case([int(n) for n in rng.integers(0, 400, 40)], 4, kv8, 16, seed=8, values="ties")
+    d = _run(x, 150, 20)
+    hs2.hs2_sync()
+    _check(x, d, 150, 20)
+
+
 @pytest.mark.parametrize("values", ["ties", "equal", "wild"])
 @pytest.mark.parametrize("n,keep,recent", [(4099, 1000, 64), (9000, 4500, 0)])
 def test_ties_signs_and_ranges(values, n, keep, recent):

@@ -27,14 +27,14 @@
 
 namespace hs2 {
 
-constexpr int EV_THREADS = 512;
+constexpr int EV_THREADS = 1024;      // of a CTA that has an SM to itself
+constexpr int EV_THREADS_MANY = 512;  // where there are more rows than SMs: two CTAs an SM overlap
 constexpr int EV_MAX_CTAS = 8;  // CTAs of a cluster
 constexpr int EV_BINS = 2048;
 constexpr int EV_COARSE = 64;   // groups of 32 bins
 constexpr int EV_ROWS = 8;      // 16-byte pieces in flight per thread
 constexpr int EV_MAX_PART = 40960;  // keys a CTA holds in shared memory
 constexpr int EV_MAX_TABLE = 8192;  // page table entries held there
-static_assert(EV_THREADS == SEL_THREADS, "block_excl_scan");
 
 struct EvictParams {
   int Hkv, page_log2, n_pages, max_pages, keep, recent, part_cap, table_cap;
@@ -51,8 +51,8 @@ struct EvictParams {
 struct EvictSmem {
   uint32_t hist[3][EV_BINS];      // this CTA's counts of each pass, read by the other CTAs
   uint32_t coarse[3][EV_COARSE];  // the same, 32 bins together
-  uint32_t part[EV_THREADS];
-  uint32_t warp_gt[16], warp_eq[16];
+  uint32_t part[EV_MAX_CTAS * EV_COARSE];
+  uint32_t warp_gt[32], warp_eq[32];
   uint32_t cta_gt, cta_eq;    // read by the other CTAs
   uint32_t sh[2];
   uint32_t keys[];  // this CTA's part of the row, then its page table
@@ -60,10 +60,10 @@ struct EvictSmem {
 
 // Sums BINS counts over the cluster and finds the bin that holds rank k from the
 // top down: out = (bin, count in the bins above it).  BINS is 32 or 64.
-template <int BINS>
+template <int THREADS, int BINS>
 __device__ __forceinline__ void ev_find(cooperative_groups::cluster_group& cl, uint32_t* counts, int ctas, uint32_t k,
                                         uint32_t* part, uint32_t* out) {
-  static_assert(EV_THREADS / BINS >= EV_MAX_CTAS, "a thread reads one count");
+  static_assert(THREADS / BINS >= EV_MAX_CTAS && BINS <= EV_COARSE, "a thread reads one count");
   const int tid = threadIdx.x, bin = tid % BINS, r = tid / BINS;
   if (r < EV_MAX_CTAS) part[tid] = r < ctas ? cl.map_shared_rank(counts, r)[bin] : 0u;
   __syncthreads();
@@ -96,8 +96,8 @@ __device__ __forceinline__ void ev_find(cooperative_groups::cluster_group& cl, u
   __syncthreads();
 }
 
-template <bool KV8>
-__global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictParams p) {
+template <bool KV8, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) cache_evict_kernel(const EvictParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ __align__(16) uint8_t ev_raw[];
@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
   }
   if (rank == 0 && g == 0 && tid == 0) p.new_len[b] = min(n, p.keep);
   if (n <= p.keep) {
-    for (int i = rank * EV_THREADS + tid; i < p.keep; i += ctas * EV_THREADS) idx[i] = i < n ? i : -1;
+    for (int i = rank * THREADS + tid; i < p.keep; i += ctas * THREADS) idx[i] = i < n ? i : -1;
     if (acc_out && acc_out != acc)
-      for (int i = rank * EV_THREADS + tid; i < n; i += ctas * EV_THREADS) acc_out[i] = acc[i];
+      for (int i = rank * THREADS + tid; i < n; i += ctas * THREADS) acc_out[i] = acc[i];
     return;
   }
 
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
     const int pages = (n + (1 << p.page_log2) - 1) >> p.page_log2;
     if (pages <= p.table_cap) {
       int32_t* held_table = reinterpret_cast<int32_t*>(sm.keys + p.part_cap);
-      for (int i = tid; i < pages; i += EV_THREADS) held_table[i] = table[i];
+      for (int i = tid; i < pages; i += THREADS) held_table[i] = table[i];
       table = held_table;  // read after the cluster's barriers below
     }
   }
@@ -145,13 +145,13 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
   if (k > 0) {
     if (held) {
       const float4* a4 = reinterpret_cast<const float4*>(acc + lo);
-      for (int i = tid; i < (cnt + 3) / 4; i += EV_THREADS) {
+      for (int i = tid; i < (cnt + 3) / 4; i += THREADS) {
         const float4 x = a4[i];  // the tail stays inside the row: acc_stride is a multiple of 4
         reinterpret_cast<uint4*>(sm.keys)[i] =
             make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
       }
     }
-    for (int i = tid; i < 3 * EV_BINS / 4; i += EV_THREADS)
+    for (int i = tid; i < 3 * EV_BINS / 4; i += THREADS)
       reinterpret_cast<uint4*>(sm.hist[0])[i] = make_uint4(0, 0, 0, 0);
     uint32_t prefix = 0, pmask = 0;
     krem = static_cast<uint32_t>(k);
@@ -161,12 +161,12 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
       const uint32_t dmask = pass == 2 ? 1023u : 2047u;
       uint32_t* hist = sm.hist[pass];
       __syncthreads();
-      for (int i = tid; i < cnt; i += EV_THREADS) {
+      for (int i = tid; i < cnt; i += THREADS) {
         const uint32_t key = key_at(i);
         if ((key & pmask) == prefix) atomicAdd(&hist[(key >> shift) & dmask], 1u);
       }
       __syncthreads();
-      {  // groups of 32 bins: eight lanes add up four bins each
+      if (tid < EV_BINS / 4) {  // groups of 32 bins: eight lanes add up four bins each
         const uint4 x = reinterpret_cast<const uint4*>(hist)[tid];
         uint32_t c = (x.x + x.y) + (x.z + x.w);
         c += __shfl_xor_sync(0xffffffffu, c, 1);
@@ -177,10 +177,10 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
       cl.sync();  // each pass has counts of its own, so one barrier a pass is enough
       // the group that holds rank krem from the top, then the bin in it; both
       // from the sums over the cluster, so that few words cross it
-      ev_find<EV_COARSE>(cl, sm.coarse[pass], ctas, krem, sm.part, sm.sh);
+      ev_find<THREADS, EV_COARSE>(cl, sm.coarse[pass], ctas, krem, sm.part, sm.sh);
       const uint32_t group = sm.sh[0], above = sm.sh[1];
       __syncthreads();
-      ev_find<32>(cl, hist + 32 * group, ctas, krem - above, sm.part, sm.sh);
+      ev_find<THREADS, 32>(cl, hist + 32 * group, ctas, krem - above, sm.part, sm.sh);
       if (tid == 0) {
         sm.sh[0] += 32 * group;
         sm.sh[1] += above;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
     T = prefix;
 
     // ---- list: warp w owns [w * piece, (w + 1) * piece) of this CTA's part
-    const int piece = ((cnt + EV_THREADS / 32 - 1) / (EV_THREADS / 32) + 31) & ~31;
+    const int piece = ((cnt + THREADS / 32 - 1) / (THREADS / 32) + 31) & ~31;
     const int w_lo = min(cnt, warp * piece), w_hi = min(cnt, w_lo + piece);
     uint32_t gt = 0, eq = 0;
     for (int i = w_lo + lane; i < w_hi; i += 32) {
@@ -208,24 +208,26 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
       sm.warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t a = 0, c = 0;
-      for (int w = 0; w < EV_THREADS / 32; ++w) {
-        a += sm.warp_gt[w];
-        c += sm.warp_eq[w];
+    if (warp == 0) {
+      const bool own = lane < THREADS / 32;
+      const uint32_t a = __reduce_add_sync(0xffffffffu, own ? sm.warp_gt[lane] : 0u);
+      const uint32_t c = __reduce_add_sync(0xffffffffu, own ? sm.warp_eq[lane] : 0u);
+      if (lane == 0) {
+        sm.cta_gt = a;
+        sm.cta_eq = c;
       }
-      sm.cta_gt = a;
-      sm.cta_eq = c;
     }
     cl.sync();
-    // counts before this warp's piece: lanes 0-15 the CTA's warps, 16 on the CTAs
+    // counts before this warp's piece: the CTA's warps and the cluster's CTAs before
+    static_assert(THREADS <= 32 * 32, "a lane per warp");
     uint32_t gt_before = 0, eq_before = 0;
     if (lane < warp) {
       gt_before = sm.warp_gt[lane];
       eq_before = sm.warp_eq[lane];
-    } else if (lane >= 16 && lane - 16 < rank) {
-      gt_before = *cl.map_shared_rank(&sm.cta_gt, lane - 16);
-      eq_before = *cl.map_shared_rank(&sm.cta_eq, lane - 16);
+    }
+    if (lane < rank) {
+      gt_before += *cl.map_shared_rank(&sm.cta_gt, lane);
+      eq_before += *cl.map_shared_rank(&sm.cta_eq, lane);
     }
     gt_before = __reduce_add_sync(0xffffffffu, gt_before);
     eq_before = __reduce_add_sync(0xffffffffu, eq_before);
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
     }
   }
   if (rank == ctas - 1)
-    for (int i = tid; i < p.recent; i += EV_THREADS) idx[k + i] = n - p.recent + i;
+    for (int i = tid; i < p.recent; i += THREADS) idx[k + i] = n - p.recent + i;
   cl.sync();  // the list is complete; no CTA reads another's shared memory any more
 
   // ---- move: batches of rows, in ascending order, by the whole cluster
@@ -259,10 +261,10 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
   };
   const int piece = tid % PIECES;
   uint8_t* base = (piece < PIECES / 2 ? p.k : p.v) + static_cast<int64_t>(g) * p.head_b + (piece % (PIECES / 2)) * 16;
-  const int step = ctas * (EV_THREADS / PIECES);  // rows the cluster's threads cover at once
-  const int row0 = rank * (EV_THREADS / PIECES) + tid / PIECES;
+  const int step = ctas * (THREADS / PIECES);  // rows the cluster's threads cover at once
+  const int row0 = rank * (THREADS / PIECES) + tid / PIECES;
   const int batch = step * EV_ROWS;
-  const int ctid = rank * EV_THREADS + tid;  // scalars of row ctid of a batch
+  const int ctid = rank * THREADS + tid;  // scalars of row ctid of a batch
   int old[EV_ROWS];  // old positions of the batch's rows, read a batch ahead
   auto olds_of = [&](int i0) {
 #pragma unroll
@@ -272,6 +274,8 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
     }
   };
   olds_of(0);
+  auto scalar_of = [&](int i0) { return ctid < batch && i0 + ctid < p.keep ? idx[i0 + ctid] : -1; };
+  int was_next = scalar_of(0);
   for (int i0 = 0; i0 < p.keep; i0 += batch) {
     uint4 data[EV_ROWS];
     uint32_t have = 0;
@@ -288,10 +292,9 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
     olds_of(i0 + batch);
     float x_acc = 0.f, x_ks = 0.f, x_vs = 0.f;
     int64_t from = -1;
-    const int is = i0 + ctid;
-    const bool scalar = ctid < batch && is < p.keep;
-    if (scalar) {
-      const int was = idx[is];
+    const int is = i0 + ctid, was = was_next;
+    was_next = scalar_of(i0 + batch);
+    if (was >= 0) {
       x_acc = acc[was];
       if (KV8 && (from = token_of(was)) >= 0) {
         x_ks = p.ksc[from * p.Hkv + g];
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
         if (tok >= 0) *reinterpret_cast<uint4*>(base + tok * p.tok_b) = data[e];
       }
     }
-    if (scalar) {
+    if (was >= 0) {
       if (acc_out) acc_out[is] = x_acc;
       if (KV8 && from >= 0) {
         const int64_t to = token_of(is);
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(EV_THREADS, 2) cache_evict_kernel(const EvictP
   }
   // acc_out may be acc: every kept weight is read by now
   if (acc_out)
-    for (int i = p.keep + ctid; i < n; i += ctas * EV_THREADS) acc_out[i] = 0.f;
+    for (int i = p.keep + ctid; i < n; i += ctas * THREADS) acc_out[i] = 0.f;
 }
 
 }  // namespace hs2

@@ -195,8 +195,7 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRope
         const float scale = a > 0.f ? a / 448.0f : 1.0f;
         if (cached) {
           uint32_t c[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) c[e] = e4m3x2_from_f32(x[2 * e] / scale, x[2 * e + 1] / scale);
+          e4m3_codes(x, scale, c);
           *reinterpret_cast<uint2*>((is_v ? p.vc : p.kc) + at) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
           if (l == 0) (is_v ? p.vsc : p.ksc)[slot * p.Hkv + g] = scale;
         }

@@ -28,6 +28,39 @@ __device__ __forceinline__ uint32_t e4m3x2_from_f32(float lo, float hi) {
   return c;
 }
 
+// The codes of eight values of a row, e4m3(v / scale), in pairs.
+__device__ __forceinline__ void e4m3_codes(const float (&v)[8], float scale, uint32_t (&c)[4]) {
+  if (scale >= 0x1p-90f) {
+    // x / scale, correctly rounded, without a division per value:
+    // Markstein's method (P. Markstein, "Computation of elementary
+    // functions on the IBM RISC System/6000 processor", IBM J. Res. Dev.
+    // 34(1), 1990) with y = RN(1 / scale) once per row, q = RN(x y), then
+    // q = RN(q + RN(x - q scale) y) by two FMAs, on value pairs.  For bf16
+    // rows exact rational arithmetic over every pair of mantissas of x and of
+    // the row's amax gives RN(x / scale) (tests/test_markstein_division.py;
+    // exponents shift every quantity alike while all stay normal, and the
+    // scale bound keeps the residuals normal for every quotient above
+    // 2^-12, below which both round to a zero code); for other fp32 rows the
+    // quotient is within a unit of its last place, far inside a code's step.
+    const float y = __frcp_rn(scale);
+    const uint64_t y2 = f2_pack(y, y), ns2 = f2_pack(-scale, -scale);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t x2 = f2_pack(v[2 * q], v[2 * q + 1]);
+      uint64_t q2 = f2_mul(x2, y2);
+      q2 = f2_fma(f2_fma(q2, ns2, x2), y2, q2);
+      float q0, q1;
+      f2_unpack(q2, q0, q1);
+      // the quotient has x's sign; the correction's RN(+0 + -0) = +0
+      // would lose it for x = -0
+      c[q] = e4m3x2_from_f32(copysignf(q0, v[2 * q]), copysignf(q1, v[2 * q + 1]));
+    }
+  } else {  // rows of amax below 448 * 2^-90: the IEEE division
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[q] = e4m3x2_from_f32(v[2 * q] / scale, v[2 * q + 1] / scale);
+  }
+}
+
 // A half-warp covers one row with 16-byte loads (8 values per lane); each warp
 // issues the loads of 8 rows before converting any, to keep bytes in flight.
 __global__ void __launch_bounds__(256) quantize_kv_kernel(const QuantParams p) {
@@ -65,34 +98,7 @@ __global__ void __launch_bounds__(256) quantize_kv_kernel(const QuantParams p) {
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));  // within the half-warp
       const float scale = (a > 0.f) ? a / 448.0f : 1.0f;
       uint32_t c[4];
-      if (scale >= 0x1p-90f) {
-        // x / scale, correctly rounded, without a division per value:
-        // Markstein's method (P. Markstein, "Computation of elementary
-        // functions on the IBM RISC System/6000 processor", IBM J. Res. Dev.
-        // 34(1), 1990) with y = RN(1 / scale) once per row, q = RN(x y), then
-        // q = RN(q + RN(x - q scale) y) by two FMAs, on value pairs.  Exact
-        // rational arithmetic over every pair of bf16 mantissas of x and of
-        // the row's amax gives RN(x / scale) (tests/test_markstein_division.py;
-        // exponents shift every quantity alike while all stay normal, and the
-        // scale bound keeps the residuals normal for every quotient above
-        // 2^-12, below which both round to a zero code).
-        const float y = __frcp_rn(scale);
-        const uint64_t y2 = f2_pack(y, y), ns2 = f2_pack(-scale, -scale);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint64_t x2 = f2_pack(v[2 * q], v[2 * q + 1]);
-          uint64_t q2 = f2_mul(x2, y2);
-          q2 = f2_fma(f2_fma(q2, ns2, x2), y2, q2);
-          float q0, q1;
-          f2_unpack(q2, q0, q1);
-          // the quotient has x's sign; the correction's RN(+0 + -0) = +0
-          // would lose it for x = -0
-          c[q] = e4m3x2_from_f32(copysignf(q0, v[2 * q]), copysignf(q1, v[2 * q + 1]));
-        }
-      } else {  // rows of amax below 448 * 2^-90: the IEEE division
-#pragma unroll
-        for (int q = 0; q < 4; ++q) c[q] = e4m3x2_from_f32(v[2 * q] / scale, v[2 * q + 1] / scale);
-      }
+      e4m3_codes(v, scale, c);
       if (rowi[k] < p.rows) {
         const int t = rowi[k] / p.Hkv;
         const int hd = rowi[k] - t * p.Hkv;

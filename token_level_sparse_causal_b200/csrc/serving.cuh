@@ -150,8 +150,36 @@ int launch_norm_rope(const NormRopeParams& p, bool kv8, bool pairs, cudaStream_t
   return launched();
 }
 
+// Clusters of `ctas` CTAs of cache_evict_kernel that run at once on the current
+// device (a GPC's SMs are shared out in whole clusters), asked once per device.
+int active_clusters(int ctas) {
+  static std::mutex mu;
+  static int known[128][EV_MAX_CTAS + 1];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[dev][ctas];
+  if (n == 0) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(EV_THREADS);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, cache_evict_kernel<false, EV_THREADS>, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sm_count() / ctas;
+    }
+  }
+  return n;
+}
+
 template <typename K>
-int launch_evict(K kernel, const EvictParams& p, const hs2_cache* c, int ctas, uint32_t smem, cudaStream_t st) {
+int launch_evict(K kernel, const EvictParams& p, const hs2_cache* c, int ctas, int threads, uint32_t smem,
+                 cudaStream_t st) {
   if (int rc = set_smem(kernel, smem)) return rc;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -159,7 +187,7 @@ int launch_evict(K kernel, const EvictParams& p, const hs2_cache* c, int ctas, u
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(c->Hkv), static_cast<unsigned>(c->n_seqs));
-  cfg.blockDim = dim3(EV_THREADS);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &attr;
@@ -297,11 +325,13 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   p.acc_stride = acc_stride;
   p.idx = idx;
   p.new_len = new_len;
-  // CTAs a row: as many as run at once (two an SM), up to a portable cluster
-  // (clusters of 16 ran one a GPC and took longer)
+  // CTAs a row: as many as let every row run at once, up to a portable cluster
+  // (16 rows of 131072 positions: two waves of clusters of 8 took 82 us, one of
+  // clusters of 6 takes 54).  More rows than SMs: smaller CTAs, two an SM (256
+  // rows of 2000: 69 us against 84).
   const int64_t rows = static_cast<int64_t>(cache->n_seqs) * cache->Hkv;
   int ctas = EV_MAX_CTAS;
-  while (ctas > 1 && rows * ctas > 2 * sm_count()) ctas /= 2;
+  while (ctas > 1 && rows > active_clusters(ctas)) --ctas;
   // shared memory for the longest part a row of this cache can have, and its pages
   const int64_t longest = std::min<int64_t>(acc_stride, static_cast<int64_t>(cache->max_pages) * cache->page);
   const int64_t part = ((longest + ctas - 1) / ctas + 3) & ~int64_t(3);
@@ -309,8 +339,12 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   p.table_cap = std::min(cache->max_pages, EV_MAX_TABLE);
   const uint32_t smem = static_cast<uint32_t>(sizeof(EvictSmem)) + static_cast<uint32_t>(p.part_cap + p.table_cap) * 4u;
   const Range range("hs2 cache_evict");
-  return kv8 ? launch_evict(cache_evict_kernel<true>, p, cache, ctas, smem, static_cast<cudaStream_t>(stream))
-             : launch_evict(cache_evict_kernel<false>, p, cache, ctas, smem, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows > active_clusters(1))
+    return kv8 ? launch_evict(cache_evict_kernel<true, EV_THREADS_MANY>, p, cache, ctas, EV_THREADS_MANY, smem, st)
+               : launch_evict(cache_evict_kernel<false, EV_THREADS_MANY>, p, cache, ctas, EV_THREADS_MANY, smem, st);
+  return kv8 ? launch_evict(cache_evict_kernel<true, EV_THREADS>, p, cache, ctas, EV_THREADS, smem, st)
+             : launch_evict(cache_evict_kernel<false, EV_THREADS>, p, cache, ctas, EV_THREADS, smem, st);
 }
 
 int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const void* v, const int32_t* cu_q,
