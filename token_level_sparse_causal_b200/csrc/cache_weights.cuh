@@ -45,7 +45,7 @@ struct WeightBars {
   uint64_t rows_ready[2];
   uint64_t fin;
   int first, count;   // as in TreeBars; a unit is a (sequence, KV head) here
-  int b, unit, tile;
+  int b, unit, offset, row0, T, ctx;
   int each, more;
   uint32_t tmem_slot;
   int abort;
@@ -72,6 +72,9 @@ struct WeightWalk {
   int left;
   __device__ __forceinline__ void load(const TreeParams& p) {
     tree_seq(p, b, row0, T, ctx);
+    sizes(p);
+  }
+  __device__ __forceinline__ void sizes(const TreeParams& p) {
     tiles = T ? (ctx + T + 127) >> 7 : 0;
     mtiles = (T + p.R - 1) / p.R;
   }
@@ -81,8 +84,11 @@ struct WeightWalk {
     b = bars->b;
     g = bars->unit;
     m = 0;
-    load(p);
-    t0 = bars->tile;
+    row0 = bars->row0;
+    T = bars->T;
+    ctx = bars->ctx;
+    sizes(p);
+    t0 = bars->offset;
     t1 = min(tiles, t0 + left);
     return true;
   }
@@ -151,7 +157,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     tmem_alloc(&bars->tmem_slot, 256);
     tmem_relinquish();
   }
-  if (warp == 2) tree_split(p, bars, false, 901);
+  if (warp == 2) tree_split(p, bars, false, 0, 901);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -213,8 +213,8 @@ int launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap&
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(rows, 32)));
+  cfg.blockDim = dim3(32 * TM_WARPS);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -43,6 +43,7 @@ namespace hs2 {
 
 constexpr int TR_MAX_ITEMS = 6;  // tiles of 32 KB in the ring, at most
 constexpr int TR_MAX_RAW = 5;    // e4m3: raw tiles of 16 KB, at most
+constexpr int TR_OVERHEAD = 3;   // what a unit costs beside its key tiles, in tiles (see tree_split)
 constexpr int TR_SCALES = 8;     // e4m3: key tiles whose scales are held or on their way
 constexpr uint32_t RAW_BYTES = 128u * 128u;
 constexpr int TR_CONV = 256;     // e4m3: converting threads
@@ -60,7 +61,7 @@ struct TreeParams {
   float* lse;
   float* part_o;    // [CTA][2][128][128], un-normalised
   float2* part_ml;  // [CTA][2][128]
-  int4* part_unit;  // [CTA]: (sequence, KV head, tile, last CTA) of the unit whose first part this CTA holds
+  int4* part_unit;  // [CTA]: (first row, tokens, KV head, last CTA) of the unit whose first part this CTA holds
   uint64_t limit_ns;
   uint32_t flags;
 };
@@ -75,13 +76,15 @@ struct TreeBars {
   uint64_t ml_ready, o_free;
   uint64_t x_ready[2], x_free[2];  // the exchange of O between row blocks, per warpgroup
   uint64_t fin;
-  int first, count;   // this CTA's stretch: first tile, number of tiles
-  int b, unit, tile;  // where the stretch begins
-  int each, more;     // tiles of a CTA; the first `more` CTAs have one more
+  int first, count;          // this CTA's stretch, in units of a key tile's cost
+  int b, unit, offset;       // where it begins: sequence, its unit, cost inside the unit
+  int row0, T, ctx;          // its sequence
+  int each, more;     // cost of a CTA; the first `more` CTAs have one more
   uint32_t tmem_slot;
   int abort;
 };
-static_assert(sizeof(TreeBars) <= 512, "barrier area");
+constexpr uint32_t TR_BAR_BYTES = 640;
+static_assert(sizeof(TreeBars) <= TR_BAR_BYTES, "barrier area");
 
 // RB: rows of a block (32, 64 or 128); a unit has RB / G tokens.
 template <bool KV8, int RB>
@@ -94,7 +97,7 @@ struct TreeSmem {
   static constexpr uint32_t RAW = ITEM + ITEMS * TILE_BYTES;
   static constexpr uint32_t SCALE = RAW + (KV8 ? RAWS * RAW_BYTES : 0u);
   static constexpr uint32_t BAR = SCALE + (KV8 ? TR_SCALES * 1024u : 0u);
-  static constexpr uint32_t ML = BAR + 512u;     // float2 [2][128]
+  static constexpr uint32_t ML = BAR + TR_BAR_BYTES;     // float2 [2][128]
   static constexpr uint32_t EXCH = ML + 2048u;   // float [2][128 - RB][32]
   static constexpr uint32_t BYTES = EXCH + 2u * (128 - RB) * 128u;
   static_assert(BYTES <= 232448u, "shared memory of one CTA");
@@ -118,29 +121,40 @@ struct TreeWalk {
   int row0, T, ctx;     // its sequence
   int tiles, mtiles;    // key tiles of the unit, token tiles of the sequence
   int t0, t1;           // the segment's key tiles
-  int left, pos;        // tiles left in the stretch, global index of t0
+  int left, pos;        // cost left in the stretch from the unit's begin on, and where that lies in all
 
   __device__ __forceinline__ void load(const TreeParams& p) {
     tree_seq(p, b, row0, T, ctx);
+    sizes(p);
+  }
+  __device__ __forceinline__ void sizes(const TreeParams& p) {
     tiles = T ? (ctx + T + 127) >> 7 : 0;
-    mtiles = (T + p.R - 1) / p.R;
+    mtiles = T <= p.R ? (T > 0 ? 1 : 0) : (T + p.R - 1) / p.R;
   }
   __device__ __forceinline__ bool begin(const TreeParams& p, const TreeBars* bars) {
     left = bars->count;
     if (left <= 0) return false;
     pos = bars->first;
     b = bars->b;
-    load(p);
-    g = bars->unit / mtiles;
-    m = bars->unit % mtiles;
-    t0 = bars->tile;
-    t1 = min(tiles, t0 + left);
-    return true;
+    row0 = bars->row0;
+    T = bars->T;
+    ctx = bars->ctx;
+    sizes(p);
+    g = mtiles == 1 ? bars->unit : bars->unit / mtiles;
+    m = bars->unit - g * mtiles;
+    const int f = bars->offset;
+    pos = bars->first - f;
+    left = bars->count + f;
+    t0 = max(0, f - TR_OVERHEAD);
+    t1 = min(tiles, left - TR_OVERHEAD);
+    return t1 > t0 || advance(p);
   }
-  __device__ __forceinline__ bool next(const TreeParams& p) {
-    left -= t1 - t0;
-    pos += t1 - t0;
-    if (left <= 0) return false;
+  // to the next unit of which the stretch holds a tile
+  __device__ __forceinline__ bool next(const TreeParams& p) { return advance(p); }
+  __device__ __forceinline__ bool advance(const TreeParams& p) {
+    left -= TR_OVERHEAD + tiles;
+    pos += TR_OVERHEAD + tiles;
+    if (left <= TR_OVERHEAD) return false;  // the next unit's first tile is the next CTA's
     if (++m == mtiles) {
       m = 0;
       if (++g == p.Hkv) {
@@ -148,13 +162,15 @@ struct TreeWalk {
         do {
           ++b;
           load(p);
-        } while (T == 0);  // tiles are left, so a sequence with some follows
+        } while (T == 0);  // cost is left, so a sequence with some follows
       }
     }
     t0 = 0;
-    t1 = min(tiles, left);
+    t1 = min(tiles, left - TR_OVERHEAD);
     return true;
   }
+  // the stretch ends with this unit, or inside it
+  __device__ __forceinline__ bool last() const { return left <= 2 * TR_OVERHEAD + tiles; }
   __device__ __forceinline__ int n() const { return t1 - t0; }
   __device__ __forceinline__ int rows(const TreeParams& p) const { return min(p.R, T - m * p.R) * p.G; }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
@@ -162,30 +178,37 @@ struct TreeWalk {
   __device__ __forceinline__ int last_rows() const { return t1 == tiles ? ctx + T - (tiles - 1) * 128 : 128; }
 };
 
-// A lane's share of a split: the key tiles of sequence b's units.
-__device__ __forceinline__ int64_t tree_cost(const TreeParams& p, int b, bool units, int where) {
-  if (b >= p.B) return 0;
-  int row0, T, ctx;
-  if (!tree_seq(p, b, row0, T, ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
-  return T ? static_cast<int64_t>((ctx + T + 127) >> 7) * p.Hkv * (units ? (T + p.R - 1) / p.R : 1) : 0;
-}
-
-// One warp splits all tiles evenly over the CTAs and finds where this CTA's
-// stretch begins.  units: sequences are counted once per token tile.
+// One warp splits all key tiles evenly over the CTAs and finds where this CTA's
+// stretch begins.  units: a sequence's keys count once per token tile.  over:
+// cost of a unit beside its tiles (queries to load, a pipeline to fill, an O to
+// write); without it the CTAs with many short sequences came in last.
 template <typename Bars>
-__device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool units, int where) {
+__device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool units, int over, int where) {
   const int lane = threadIdx.x & 31;
-  const int64_t mine = tree_cost(p, lane, units, where);  // the first 32 sequences, used twice
-  int64_t total64 = mine;
-  for (int b = lane + 32; b < p.B; b += 32) total64 += tree_cost(p, b, units, where);
+  struct Seq {
+    int row0, T, ctx;
+    int64_t cost;
+  };
+  auto look = [&](int b) {
+    Seq q{0, 0, 0, 0};
+    if (b < p.B) {
+      if (!tree_seq(p, b, q.row0, q.T, q.ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
+      const int mtiles = !units || q.T <= p.R ? 1 : (q.T + p.R - 1) / p.R;
+      if (q.T) q.cost = static_cast<int64_t>(((q.ctx + q.T + 127) >> 7) + over) * (p.Hkv * mtiles);
+    }
+    return q;
+  };
+  const Seq mine = look(lane);  // the first 32 sequences, used twice
+  int64_t total64 = mine.cost;
+  for (int b = lane + 32; b < p.B; b += 32) total64 += look(b).cost;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total64 += __shfl_xor_sync(0xffffffffu, total64, o);
   if (total64 > 0x7fffffff) {  // beyond any cache; no part of it is done
     if (lane == 0 && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
     total64 = 0;
   }
-  const int total = static_cast<int>(total64);
-  const int each = total / static_cast<int>(gridDim.x), more = total - each * static_cast<int>(gridDim.x);
+  const unsigned total = static_cast<unsigned>(total64), ctas = gridDim.x;
+  const int each = static_cast<int>(total / ctas), more = static_cast<int>(total % ctas);
   const int c = blockIdx.x;
   const int first = c * each + min(c, more), count = each + (c < more ? 1 : 0);
   if (lane == 0) {
@@ -197,7 +220,8 @@ __device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool
   if (count == 0) return;
   int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int w = static_cast<int>(b0 == 0 ? mine : tree_cost(p, b0 + lane, units, where));
+    const Seq q = b0 == 0 ? mine : look(b0 + lane);
+    const int w = static_cast<int>(q.cost);
     int incl = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -206,13 +230,14 @@ __device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool
     }
     const bool here = first >= before + incl - w && first < before + incl;
     if (here) {
-      int row0, T, ctx;
-      tree_seq(p, b0 + lane, row0, T, ctx);
-      const int tiles = (ctx + T + 127) >> 7;
-      const int rest = first - (before + incl - w);
+      const unsigned cost = (static_cast<unsigned>(q.ctx + q.T + 127) >> 7) + over;
+      const unsigned rest = static_cast<unsigned>(first - (before + incl - w)), unit = rest / cost;
       bars->b = b0 + lane;
-      bars->unit = rest / tiles;
-      bars->tile = rest % tiles;
+      bars->unit = static_cast<int>(unit);
+      bars->offset = static_cast<int>(rest - unit * cost);
+      bars->row0 = q.row0;
+      bars->T = q.T;
+      bars->ctx = q.ctx;
     }
     if (__any_sync(0xffffffffu, here)) return;
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -328,51 +353,59 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     return;
   }
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < ITEMS; ++s) {
-      mbar_init(&bars->full[s], KV8 ? TR_CONV / 32 : 1);
-      mbar_init(&bars->empty[s], 1);
-      mbar_init(&bars->v_raw[s], 1);
-    }
-    if (KV8) {
-      for (int s = 0; s < RAWS; ++s) {
-        mbar_init(&bars->raw_full[s], 1);
-        mbar_init(&bars->raw_empty[s], TR_CONV / 32);
+  // Warp 0 sets up the barriers, finds the stretch and goes straight on to its
+  // loads (it arrives at the CTA's barrier without waiting there).
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int s = 0; s < ITEMS; ++s) {
+        mbar_init(&bars->full[s], KV8 ? TR_CONV / 32 : 1);
+        mbar_init(&bars->empty[s], 1);
+        mbar_init(&bars->v_raw[s], 1);
       }
-      for (int s = 0; s < TR_SCALES; ++s) {
-        mbar_init(&bars->sc_full[s], 32);
-        mbar_init(&bars->sc_empty[s], 4);
+      if (KV8) {
+        for (int s = 0; s < RAWS; ++s) {
+          mbar_init(&bars->raw_full[s], 1);
+          mbar_init(&bars->raw_empty[s], TR_CONV / 32);
+        }
+        for (int s = 0; s < TR_SCALES; ++s) {
+          mbar_init(&bars->sc_full[s], 32);
+          mbar_init(&bars->sc_empty[s], 4);
+        }
       }
+      mbar_init(&bars->q_full, 1);
+      mbar_init(&bars->q_empty, 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&bars->s_full[x], 1);
+        mbar_init(&bars->p_ready[x], 4);
+        mbar_init(&bars->o_done[x], 1);
+      }
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&bars->x_ready[x], RB < 128 ? 4 - RB / 32 : 1);
+        mbar_init(&bars->x_free[x], RB / 32);
+      }
+      mbar_init(&bars->ml_ready, 8);
+      mbar_init(&bars->o_free, 8);
+      mbar_init(&bars->fin, 1);
+      bars->abort = 0;
+      fence_mbar_init();
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
     }
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_ready[x], 4);
-      mbar_init(&bars->o_done[x], 1);
+    __syncwarp();
+    tree_split(p, bars, true, TR_OVERHEAD, 801);
+    __syncwarp();
+    asm volatile("bar.arrive 1, %0;" ::"n"(tr_threads(KV8)) : "memory");
+  } else {
+    if (warp == 1) {
+      tmem_alloc(&bars->tmem_slot, 512);
+      tmem_relinquish();
     }
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars->x_ready[x], RB < 128 ? 4 - RB / 32 : 1);
-      mbar_init(&bars->x_free[x], RB / 32);
-    }
-    mbar_init(&bars->ml_ready, 8);
-    mbar_init(&bars->o_free, 8);
-    mbar_init(&bars->fin, 1);
-    bars->abort = 0;
-    fence_mbar_init();
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(tr_threads(KV8)) : "memory");
+    tc_fence_after();
   }
-  if (warp == 1) {
-    tmem_alloc(&bars->tmem_slot, 512);
-    tmem_relinquish();
-  }
-  if (warp == 2) tree_split(p, bars, true, 801);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars->tmem_slot;
+  const uint32_t tmem = bars->tmem_slot;  // not warp 0's to read
   // Registers move to the two softmax warpgroups (a row of scores is 128 of
   // them); the shares of all warpgroups add up to no more than the CTA was
   // launched with: 2 x 208 + 88 = 3 x 168; with an e4m3 cache (640 threads of
@@ -556,12 +589,12 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       ti += n;
       ++seg;
       // the stretch's last segment may be a unit's first part
-      if (threadIdx.x == 128 && w.left == n) {
+      if (threadIdx.x == 128 && w.last()) {
         const bool head = w.t0 == 0 && w.t1 < w.tiles;
         // the CTA with the unit's last tile (its segment begins at tile 0)
-        const int end = w.pos + w.tiles - 1, big = bars->more * (bars->each + 1);
+        const int end = w.pos + TR_OVERHEAD + w.tiles - 1, big = bars->more * (bars->each + 1);
         const int last = end < big ? end / (bars->each + 1) : bars->more + (end - big) / bars->each;
-        p.part_unit[blockIdx.x] = make_int4(w.b, w.g, w.m, head ? last : -1);
+        p.part_unit[blockIdx.x] = make_int4(w.row0 + w.m * p.R, min(p.R, w.T - w.m * p.R), w.g, head ? last : -1);
       }
       if (!w.next(p)) break;
     }
@@ -821,45 +854,74 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
   }
 }
 
+// Adds a part (m, l) = q, O = v to a row's (M, L), acc.
+__device__ __forceinline__ void merge_part(float& M, float& L, float4& acc, float2 q, float4 v) {
+  const float m = fmaxf(M, q.x);
+  const float keep = M == -INFINITY ? 0.f : ex2_approx(M - m), w = q.x == -INFINITY ? 0.f : ex2_approx(q.x - m);
+  L = (M == -INFINITY ? L : L * keep) + (q.x == -INFINITY ? q.y : q.y * w);  // without a max: 0, or a NaN that stays
+  acc.x = fmaf(v.x, w, acc.x * keep);
+  acc.y = fmaf(v.y, w, acc.y * keep);
+  acc.z = fmaf(v.z, w, acc.z * keep);
+  acc.w = fmaf(v.w, w, acc.w * keep);
+  M = m;
+}
+
 // Joins the parts of the units that several CTAs share: block (c, y) takes rows
-// 4y .. 4y + 3 (one warp each) of the unit whose first part CTA c holds.
-__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeParams p) {
+// y, y + gridDim.y, ... of the unit whose first part CTA c holds.  A row's parts
+// are spread over 1, 2, 4 or 8 warps, so that a long chain of parts is read at
+// once; the warps' sums meet in shared memory, in a fixed order.
+constexpr int TM_WARPS = 8;
+__global__ void __launch_bounds__(32 * TM_WARPS) tree_merge_kernel(const TreeParams p) {
+  __shared__ float4 acc_s[TM_WARPS][32];
+  __shared__ float2 ml_s[TM_WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched beside tree_attn_kernel's end
   const int c = blockIdx.x;
   const int4 u = p.part_unit[c];
-  if (u.w < 0) return;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  int row0, T, ctx;
-  tree_seq(p, u.x, row0, T, ctx);
-  const int t = u.z * p.R + r / p.G;
-  if (r >= p.R * p.G || t >= T) return;
-  // parts in key order: slot 1 of CTA c, then slot 0 of CTAs c + 1 .. last
-  auto slot = [&](int k) { return (static_cast<int64_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * 128 + r; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = u.y * p.G;
+  if (u.w < 0 || static_cast<int>(blockIdx.y) >= rows) return;
   const int n = u.w - c + 1;
-  float M = -INFINITY;
-  for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[slot(k)].x);
+  const int per_row = n <= 2 ? 1 : n <= 4 ? 2 : n <= 8 ? 4 : 8;  // warps of a row
+  const int sub = warp / per_row, wk = warp % per_row;
+  for (int i0 = 0; static_cast<int>(blockIdx.y) + i0 * static_cast<int>(gridDim.y) < rows; i0 += TM_WARPS / per_row) {
+    const int r = blockIdx.y + (i0 + sub) * gridDim.y;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows) {
+      // parts in key order: slot 1 of CTA c, then slot 0 of CTAs c + 1 .. last
+      auto slot = [&](int k) { return (static_cast<int64_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * 128 + r; };
+      for (int k0 = wk; k0 < n; k0 += 4 * per_row) {
+        float4 v[4];
+        float2 q[4];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float2 q = p.part_ml[slot(k)];
-    const float4 v = reinterpret_cast<const float4*>(p.part_o + slot(k) * 128)[lane];
-    const float wt = q.x == -INFINITY ? 0.f : ex2_approx(q.x - M);
-    L = fmaf(q.y, wt, L);
-    acc.x = fmaf(v.x, wt, acc.x);
-    acc.y = fmaf(v.y, wt, acc.y);
-    acc.z = fmaf(v.z, wt, acc.z);
-    acc.w = fmaf(v.w, wt, acc.w);
+        for (int i = 0; i < 4; ++i) {
+          const int k = k0 + i * per_row;
+          q[i] = make_float2(-INFINITY, 0.f);
+          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < n) {
+            q[i] = p.part_ml[slot(k)];
+            v[i] = reinterpret_cast<const float4*>(p.part_o + slot(k) * 128)[lane];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) merge_part(M, L, acc, q[i], v[i]);
+      }
+    }
+    acc_s[warp][lane] = acc;
+    if (lane == 0) ml_s[warp] = make_float2(M, L);
+    __syncthreads();
+    if (wk == 0 && r < rows) {
+      for (int k = 1; k < per_row; ++k) merge_part(M, L, acc, ml_s[warp + k], acc_s[warp + k][lane]);
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const int h = u.z * p.G + r % p.G;
+      const int64_t row = u.x + r / p.G;
+      *reinterpret_cast<uint2*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + lane * 4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (lane == 0 && p.lse)
+        p.lse[static_cast<int64_t>(h) * p.n_tok + row] = (M + log2f(L)) * 0.69314718055994530942f;
+    }
+    __syncthreads();
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int h = u.y * p.G + r % p.G;
-  const int64_t row = row0 + t;
-  *reinterpret_cast<uint2*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + lane * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0 && p.lse)
-    p.lse[static_cast<int64_t>(h) * p.n_tok + row] = (M + log2f(L)) * 0.69314718055994530942f;
 }
 
 }  // namespace hs2
