@@ -26,7 +26,8 @@
 //            tile's keys (the rest of its P is zero): all warps share one row's
 //            exponentials, instead of one warp taking all of them (about 2000
 //            cycles a tile, 4500 with an e4m3 cache's scales). Each block is a
-//            softmax of its own; the epilogue adds the blocks' O;
+//            softmax of its own; the epilogue adds the blocks' O, each block a
+//            share of the columns;
 //   e4m3     codes arrive by TMA in a raw ring; eight warps turn them into bf16
 //            (exact; unlike f16 it leaves Q and P their whole range), another
 //            fetches the scales; the K scale multiplies the scores, the V
@@ -46,7 +47,7 @@ constexpr int TR_MAX_RAW = 5;    // e4m3: raw tiles of 16 KB, at most
 constexpr int TR_OVERHEAD = 3;   // what a unit costs beside its key tiles, in tiles (see tree_split)
 constexpr int TR_SCALES = 8;     // e4m3: key tiles whose scales are held or on their way
 constexpr uint32_t RAW_BYTES = 128u * 128u;
-constexpr int TR_CONV = 256;     // e4m3: converting threads
+constexpr int TR_CONV = 256;     // e4m3: converting threads (128: 229 us where 256 take 188)
 __host__ __device__ constexpr int tr_threads(bool kv8) { return 384 + (kv8 ? TR_CONV : 0); }
 
 // What a call's kernels share: the unit geometry.
@@ -380,8 +381,8 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         mbar_init(&bars->o_done[x], 1);
       }
       for (int x = 0; x < 2; ++x) {
-        mbar_init(&bars->x_ready[x], RB < 128 ? 4 - RB / 32 : 1);
-        mbar_init(&bars->x_free[x], RB / 32);
+        mbar_init(&bars->x_ready[x], 4);
+        mbar_init(&bars->x_free[x], 4);
       }
       mbar_init(&bars->ml_ready, 8);
       mbar_init(&bars->o_free, 8);
@@ -409,9 +410,9 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
   // Registers move to the two softmax warpgroups (a row of scores is 128 of
   // them); the shares of all warpgroups add up to no more than the CTA was
   // launched with: 2 x 208 + 88 = 3 x 168; with an e4m3 cache (640 threads of
-  // 96, the scores read in quarters) 2 x 128 + 3 x 72 <= 5 x 96.
+  // 96, the scores read in quarters) 2 x 136 + 3 x 64 <= 5 x 96.
   if (warp >= 4 && warp < 12) {
-    reg_acquire<KV8 ? 128 : 208>();
+    reg_acquire<KV8 ? 136 : 208>();
     // ============================================ softmax / rescale / epilogue
     const int x = (warp >= 8) ? 1 : 0;
     const int r = threadIdx.x - 128 - 128 * x;
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     const uint32_t s_tm = tmem + lane_off + x * 128;
     const uint32_t o_tm = tmem + lane_off + 256;  // O of x at + 128 x
     const int block = r / RB, row_r = r % RB;  // this thread's keys of a tile, its query row
+    constexpr int SHARE = 32 / BLOCKS;         // of 32 columns of O, those a block writes
     const int tok_r = row_r / p.G, head_r = row_r % p.G;
     // waits taken on s_full[x] and o_done[1]; segments; tiles; exchanges
     int ns = 0, no1 = 0, seg = 0, ti = 0, ex = 0;
@@ -499,6 +501,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       const float ma = ml[r].x, mb = ml[128 + r].x;
       const float wa = ma == -INFINITY ? 0.f : ex2_approx(ma - M);
       const float wb = mb == -INFINITY ? 0.f : ex2_approx(mb - M);
+      const uint64_t wa2 = f2_pack(wa, wa), wb2 = f2_pack(wb, wb);
       const bool whole = w.whole();
       const float inv = !whole ? 1.f : (L == 0.f ? 0.f : 1.f / L);
       const int64_t row = w.row0 + t;
@@ -506,74 +509,100 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 == 0 ? 1 : 0);
 #pragma unroll 1
       for (int c = 2 * x; c < 2 * x + 2; ++c) {  // this warpgroup's half of the columns
-        float v[32];
+        uint64_t v[16];
         if (warp_live) {
           uint32_t oa[32], ob[32];
           tmem_ld32(o_tm + c * 32, oa);
-          if (n > 1) tmem_ld32(o_tm + 128 + c * 32, ob);
+          if (!KV8 && n > 1) tmem_ld32(o_tm + 128 + c * 32, ob);
           tmem_ld_wait();
           reg_fence(oa);
-          if (n > 1) reg_fence(ob);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            // an O without a visible key holds nothing to add, whatever is there
-            float y = wa > 0.f ? __uint_as_float(oa[e]) * wa : 0.f;
-            if (n > 1 && wb > 0.f) y = fmaf(__uint_as_float(ob[e]), wb, y);
-            v[e] = y;
+          for (int e = 0; e < 16; ++e)
+            v[e] = f2_mul(f2_pack(__uint_as_float(oa[2 * e]), __uint_as_float(oa[2 * e + 1])), wa2);
+          if (n > 1) {
+            if (KV8) {  // fewer registers: one after the other
+              tmem_ld32(o_tm + 128 + c * 32, ob);
+              tmem_ld_wait();
+            }
+            reg_fence(ob);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v[e] = f2_fma(f2_pack(__uint_as_float(ob[2 * e]), __uint_as_float(ob[2 * e + 1])), wb2, v[e]);
           }
         }
         if (BLOCKS > 1) {
-          // the other blocks hand their part of the row to block 0 (16-byte
-          // chunks at a place XOR-ed with the row, so that eight lanes hit
-          // eight bank groups)
+          // Each block takes SHARE of the 32 columns and hands the others'
+          // theirs through shared memory: [taker][giver][row][SHARE], the
+          // 16-byte chunks XOR-ed with the row so that a store or load of
+          // eight lanes meets every bank once.
           const uint32_t area = exch_base + static_cast<uint32_t>(x * (128 - RB)) * 128u;
-          if (block > 0) {
-            if (ex > 0 && !(ok = warp_wait(&bars->x_free[x], (ex - 1) & 1, p.limit_ns, abort_flag, 846))) break;
-            if (warp_live) {
-              const uint32_t at = area + static_cast<uint32_t>(r - RB) * 128u;
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                st_shared_v4(at + ((q ^ (r & 7)) << 4),
-                             make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->x_ready[x]);
-            ++ex;
-            continue;
-          }
-          if (!(ok = warp_wait(&bars->x_ready[x], ex & 1, p.limit_ns, abort_flag, 847))) break;
+          auto place = [&](int taker, int giver) {
+            return area + static_cast<uint32_t>((taker * (BLOCKS - 1) + giver) * RB + row_r) * (SHARE * 4u);
+          };
+          auto chunk = [&](int q) {
+            return static_cast<uint32_t>(q ^ ((row_r >> (BLOCKS == 4 ? 2 : 1)) & (SHARE / 4 - 1))) << 4;
+          };
+          if (ex > 0 && !(ok = warp_wait(&bars->x_free[x], (ex - 1) & 1, p.limit_ns, abort_flag, 846))) break;
           if (warp_live) {
 #pragma unroll
-            for (int k = 1; k < BLOCKS; ++k) {
-              const uint32_t at = area + static_cast<uint32_t>((k - 1) * RB + row_r) * 128u;
+            for (int k = 0; k < BLOCKS; ++k) {  // columns SHARE k ..: to block k
+              if (k == block) continue;
+              const uint32_t at = place(k, block < k ? block : block - 1);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const uint4 y = ld_shared_v4(at + ((q ^ (row_r & 7)) << 4));
-                v[4 * q] += __uint_as_float(y.x);
-                v[4 * q + 1] += __uint_as_float(y.y);
-                v[4 * q + 2] += __uint_as_float(y.z);
-                v[4 * q + 3] += __uint_as_float(y.w);
+              for (int q = 0; q < SHARE / 4; ++q) {
+                const uint64_t lo = v[k * (SHARE / 2) + 2 * q], hi = v[k * (SHARE / 2) + 2 * q + 1];
+                st_shared_v4(at + chunk(q), make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                                                       static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)));
               }
             }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->x_ready[x]);
+          if (!(ok = warp_wait(&bars->x_ready[x], ex & 1, p.limit_ns, abort_flag, 847))) break;
+          if (warp_live) {
+            uint64_t mine[SHARE / 2];
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k)
+              if (k == block) {
+#pragma unroll
+                for (int e = 0; e < SHARE / 2; ++e) mine[e] = v[k * (SHARE / 2) + e];
+              }
+#pragma unroll
+            for (int k = 0; k < BLOCKS - 1; ++k) {
+              const uint32_t at = place(block, k);
+#pragma unroll
+              for (int q = 0; q < SHARE / 4; ++q) {
+                const uint4 y = ld_shared_v4(at + chunk(q));
+                mine[2 * q] = f2_add(mine[2 * q], f2_pack(__uint_as_float(y.x), __uint_as_float(y.y)));
+                mine[2 * q + 1] = f2_add(mine[2 * q + 1], f2_pack(__uint_as_float(y.z), __uint_as_float(y.w)));
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < SHARE / 2; ++e) v[e] = mine[e];
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->x_free[x]);
           ++ex;
         }
         if (!warp_live || !row_live) continue;
+        const int col = c * 32 + block * SHARE;  // SHARE columns from here on, in v
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + c * 32);
+          uint4* dst = reinterpret_cast<uint4*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + col);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= inv;
+          for (int q = 0; q < SHARE / 8; ++q) {
+            uint32_t o[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+            for (int e = 0; e < 4; ++e) {
+              float y0, y1;
+              f2_unpack(f2_mul(v[4 * q + e], f2_pack(inv, inv)), y0, y1);
+              o[e] = pack_bf16x2(y0, y1);
+            }
+            dst[q] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
         } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * 128 + row_r) * 128 + c * 32);
+          ulonglong2* dst = reinterpret_cast<ulonglong2*>(p.part_o + (slot * 128 + row_r) * 128 + col);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          for (int q = 0; q < SHARE / 4; ++q) dst[q] = make_ulonglong2(v[2 * q], v[2 * q + 1]);
         }
       }
       if (!ok) break;
@@ -599,7 +628,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       if (!w.next(p)) break;
     }
   } else {
-    reg_release<KV8 ? 72 : 88>();
+    reg_release<KV8 ? 64 : 88>();
     if (warp == 0) {
       // =========================================================== TMA loads
       TreeWalk w;
