@@ -3,19 +3,24 @@
 //                   exp(q_rh . k_j / sqrt(d) - lse[h][r])   (0 where j is masked)
 //
 // As kernel (2) (importance.cuh) the keys lie on the MMA's M dimension: D =
-// K tile (128 keys x d) * Q^T (d x up to 128 query rows), so TMEM lane r holds
+// K tile (128 keys x d) * Q^T (d x up to 256 query rows), so TMEM lane r holds
 // key r against every row and the thread that owns it adds its row up in
 // registers, with no reduction between threads and no atomics: each position
 // is written by one thread, in a fixed order.
 //
 // K is read once (256 B a key and KV head, 132 B as e4m3).  Work is split as
 // in tree_attn.cuh, but by (sequence, KV head): a CTA takes an equal stretch of
-// all key tiles, and for more than 128 rows walks its part of a sequence once
-// per 128 rows (adding to what it wrote; the K tiles then come from L2).  Two
-// epilogue warpgroups take the even and the odd tiles; bound by memory up to
-// about 100 rows, then by the exponentials (one per row and key, 16 a clock
-// and SM).  Exponentials run on the MUFU unit (2^-22): the cubic polynomial
-// that kernel (2) mixes in is exact only to 7.5e-5.
+// all key tiles, and for more than QR rows walks its part of a sequence once
+// per QR rows (adding to what it wrote; the K tiles then come from L2).  Of a
+// bf16 cache two pairs of epilogue warpgroups take the even and the odd tiles,
+// each warpgroup half of the columns (with one a tile 32 columns took 700
+// cycles of mostly waiting); the second hands its sums to the first through
+// shared memory.  An e4m3 cache leaves registers for one warpgroup a tile
+// beside the converting warps.  Bound by memory up to about 100 rows, then by
+// the exponentials: 16 a clock and SM on the MUFU unit, so where all 32 columns
+// of a chunk count six of its sixteen pairs take the degree-4 polynomial on the
+// FMA pipes instead (2.6e-6; the cubic that kernel (2) mixes in is exact only
+// to 7.5e-5).
 //
 // e4m3: codes arrive by TMA in a raw ring and are turned into bf16 by eight
 // warps; the key's scale multiplies its row of scores.
@@ -25,9 +30,11 @@
 
 namespace hs2 {
 
-constexpr int CW_ITEMS = 5;      // bf16: K tiles in the ring
-constexpr int CW_ITEMS_KV8 = 3;  // e4m3: converted tiles
-constexpr int CW_RAW = 5;        // e4m3: raw tiles
+constexpr int CW_MAX_ITEMS = 5;  // K tiles in the ring, at most
+constexpr int CW_MAX_RAW = 5;    // e4m3: raw tiles, at most
+constexpr int CW_CONV = 256;     // e4m3: converting threads
+__host__ __device__ constexpr int cw_halves(bool kv8) { return kv8 ? 1 : 2; }  // epilogue warpgroups of a tile
+__host__ __device__ constexpr int cw_threads(bool kv8) { return 128 + 256 * cw_halves(kv8) + (kv8 ? CW_CONV : 0); }
 
 struct WeightParams {
   TreeParams t;          // geometry, table, cu, ctx, mask, scales, limits
@@ -38,11 +45,12 @@ struct WeightParams {
 };
 
 struct WeightBars {
-  uint64_t full[CW_ITEMS], empty[CW_ITEMS];
-  uint64_t raw_full[CW_RAW], raw_empty[CW_RAW];
+  uint64_t full[CW_MAX_ITEMS], empty[CW_MAX_ITEMS];
+  uint64_t raw_full[CW_MAX_RAW], raw_empty[CW_MAX_RAW];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t rows_ready[2];
+  uint64_t part_full[2], part_empty[2];  // the second column half's sums of a tile
   uint64_t fin;
   int first, count;   // as in TreeBars; a unit is a (sequence, KV head) here
   int b, unit, offset, row0, T, ctx;
@@ -52,16 +60,22 @@ struct WeightBars {
 };
 static_assert(sizeof(WeightBars) <= 512, "barrier area");
 
-template <bool KV8>
+// QR: query rows of a pass, 128 or 256.
+template <bool KV8, int QR>
 struct WeightSmem {
-  static constexpr int ITEMS = KV8 ? CW_ITEMS_KV8 : CW_ITEMS;
-  static constexpr uint32_t ITEM = TILE_BYTES;  // after Q
+  static constexpr int ITEMS = KV8 ? (QR == 256 ? 2 : 3) : (QR == 256 ? 4 : 5);
+  static constexpr int RAWS = 5;
+  static_assert(ITEMS <= CW_MAX_ITEMS && RAWS <= CW_MAX_RAW, "rings");
+  static constexpr uint32_t QHALF = QR * 128u;
+  static constexpr uint32_t ITEM = 2 * QHALF;  // after Q
   static constexpr uint32_t RAW = ITEM + ITEMS * TILE_BYTES;
-  static constexpr uint32_t BAR = RAW + (KV8 ? CW_RAW * RAW_BYTES : 0u);
+  static constexpr uint32_t BAR = RAW + (KV8 ? RAWS * RAW_BYTES : 0u);
   // per epilogue warpgroup and segment parity, for each column (query row):
-  static constexpr uint32_t BITS = BAR + 512u;            // uint64 [2][2][128]: the drafted keys it sees
-  static constexpr uint32_t NLSE = BITS + 2 * 2 * 1024u;  // float [2][2][128]: -lse * log2(e); -inf: collects nothing
-  static constexpr uint32_t BYTES = NLSE + 2 * 2 * 512u;
+  static constexpr uint32_t BITS = BAR + 512u;                // uint64 [2][2][QR]: the drafted keys it sees
+  static constexpr uint32_t NLSE = BITS + 2 * 2 * QR * 8u;    // float [2][2][QR]: -lse * log2(e), -inf: none
+  static constexpr uint32_t LIVE = NLSE + 2 * 2 * QR * 4u;    // uint32 [2][2][QR / 32]: the columns that collect
+  static constexpr uint32_t PART = LIVE + 2 * 2 * QR / 8u;  // float [2][128]
+  static constexpr uint32_t BYTES = PART + 1024u;
   static_assert(BYTES <= 232448u, "shared memory of one CTA");
 };
 
@@ -111,12 +125,34 @@ struct WeightWalk {
   __device__ __forceinline__ int n() const { return t1 - t0; }
 };
 
-template <bool KV8>
-__global__ void __launch_bounds__(tr_threads(KV8), 1)
+// Adds 32 columns' weights of one key to sum.  ALL: every column collects, so
+// that some exponentials may leave the MUFU unit (the polynomial has no zero
+// for a column that does not; skipping such columns eight at a time cost more
+// in branches than it saved).
+template <bool ALL>
+__device__ __forceinline__ void weights_add(const uint32_t (&sr)[32], uint64_t f2, const float* nlse,
+                                            uint64_t (&sum)[4]) {
+  const float4* nl4 = reinterpret_cast<const float4*>(nlse);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float4 nl = nl4[e];  // broadcast
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = 4 * e + 2 * i, pair = 2 * e + i;
+      const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2,
+                                i ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y));
+      const bool poly = ALL && (pair % 8 == 1 || pair % 8 == 4 || pair % 8 == 6);
+      sum[pair & 3] = f2_add(sum[pair & 3], poly ? exp2_fma_x2<4>(x) : ex2_x2(x));
+    }
+  }
+}
+
+template <bool KV8, int QR>
+__global__ void __launch_bounds__(cw_threads(KV8), 1)
     cache_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const WeightParams wp) {
-  using SM = WeightSmem<KV8>;
-  constexpr int ITEMS = SM::ITEMS;
+  using SM = WeightSmem<KV8, QR>;
+  constexpr int ITEMS = SM::ITEMS, RAWS = SM::RAWS, HALVES = cw_halves(KV8);
   const TreeParams& p = wp.t;
   extern __shared__ __align__(1024) uint8_t weights_smem[];
   uint8_t* smem = weights_smem;
@@ -131,21 +167,23 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ITEMS; ++s) {
-      mbar_init(&bars->full[s], KV8 ? TR_CONV / 32 : 1);
+      mbar_init(&bars->full[s], KV8 ? CW_CONV / 32 : 1);
       mbar_init(&bars->empty[s], 1);
     }
     if (KV8) {
-      for (int s = 0; s < CW_RAW; ++s) {
+      for (int s = 0; s < RAWS; ++s) {
         mbar_init(&bars->raw_full[s], 1);
-        mbar_init(&bars->raw_empty[s], TR_CONV / 32);
+        mbar_init(&bars->raw_empty[s], CW_CONV / 32);
       }
     }
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->s_empty[x], 4);
-      mbar_init(&bars->rows_ready[x], 4);
+      mbar_init(&bars->s_empty[x], 4 * HALVES);
+      mbar_init(&bars->rows_ready[x], 4 * HALVES);
+      mbar_init(&bars->part_full[x], 4);
+      mbar_init(&bars->part_empty[x], 4);
     }
     mbar_init(&bars->fin, 1);
     bars->abort = 0;
@@ -154,7 +192,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     tma_prefetch_desc(&tmK);
   }
   if (warp == 1) {
-    tmem_alloc(&bars->tmem_slot, 256);
+    tmem_alloc(&bars->tmem_slot, 2 * QR);
     tmem_relinquish();
   }
   if (warp == 2) tree_split(p, bars, false, 0, 901);
@@ -167,7 +205,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     // ======================================================== K tiles by TMA
     WeightWalk w;
     const bool work = !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars);
-    constexpr int RING = KV8 ? CW_RAW : CW_ITEMS;
+    constexpr int RING = KV8 ? RAWS : ITEMS;
     constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
     uint64_t* full = KV8 ? bars->raw_full : bars->full;
     uint64_t* empty = KV8 ? bars->raw_empty : bars->empty;
@@ -235,7 +273,8 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-            umma_ss(tmem + x * 128, sdesc_sw128(kb + koff, 16, 1024), sdesc_sw128(q_base + koff, 16, 1024), idesc,
+            const uint32_t qoff = (kk >> 2) * SM::QHALF + (kk & 3) * 32;
+            umma_ss(tmem + x * QR, sdesc_sw128(kb + koff, 16, 1024), sdesc_sw128(q_base + qoff, 16, 1024), idesc,
                     kk > 0 ? 1u : 0u);
           }
           umma_commit(&bars->s_full[x]);
@@ -259,17 +298,19 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         if (seg > 0 && !mbar_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 931)) break;
         mbar_arrive_expect_tx(&bars->q_full, 2 * half);
         tma_load_3d(smem, &tmQ, &bars->q_full, 0, w.g * p.G, w.row0 + w.m * p.R);
-        tma_load_3d(smem + HALF_BYTES, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
+        tma_load_3d(smem + SM::QHALF, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
         ++seg;
       } while (w.next(p));
       wait_done(&bars->q_full, (seg - 1) & 1, p.limit_ns, 932);
     }
-  } else if (warp >= 4 && warp < 12) {
-    // ================= sums: thread r of warpgroup x owns key r of its tiles
-    const int x = (warp >= 8) ? 1 : 0;
-    const int r = threadIdx.x - 128 - 128 * x;
-    const uint32_t s_tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * 128;
-    int ns = 0, seg = 0;
+  } else if (warp >= 4 && warp < 4 + 8 * HALVES) {
+    // ===== sums: thread r of a warpgroup owns key r of tiles x, x + 2, ..., and
+    // all or half of the columns
+    const int x = (warp - 4) / (4 * HALVES), half = HALVES == 1 ? 0 : ((warp - 4) >> 2) & 1;
+    const int r = (threadIdx.x - 128) & 127;
+    const uint32_t s_tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * QR;
+    float* part = reinterpret_cast<float*>(smem + SM::PART) + x * 128 + r;
+    int ns = 0, seg = 0, np = 0;
     WeightWalk w;
     bool ok = w.begin(p, bars);
     while (ok) {
@@ -277,21 +318,26 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       // this segment's query rows: what each sees, and its log-sum.  A buffer is
       // written again two segments later, after every warp passed the barrier
       // of the segment between.
-      uint64_t* row_bits = reinterpret_cast<uint64_t*>(smem + SM::BITS) + (x * 2 + (seg & 1)) * 128;
-      float* row_nlse = reinterpret_cast<float*>(smem + SM::NLSE) + (x * 2 + (seg & 1)) * 128;
-      {
+      const int area = x * 2 + (seg & 1);
+      uint64_t* row_bits = reinterpret_cast<uint64_t*>(smem + SM::BITS) + area * QR;
+      float* row_nlse = reinterpret_cast<float*>(smem + SM::NLSE) + area * QR;
+      uint32_t* live = reinterpret_cast<uint32_t*>(smem + SM::LIVE) + area * (QR / 32);
+#pragma unroll
+      for (int c = 128 * half + r; c < QR; c += 128 * HALVES) {
         uint64_t bits = 0;
         float nl = -INFINITY;
-        const int t = w.m * p.R + r / p.G;
-        if (r < rows) {
+        const int t = w.m * p.R + c / p.G;
+        if (c < rows) {
           const int64_t row = w.row0 + t;
           bits = p.mask ? p.mask[row] : (2ull << t) - 1;
           if (w.T < 64) bits &= (1ull << w.T) - 1;
-          const float l = wp.lse[static_cast<int64_t>(w.g * p.G + r % p.G) * p.n_tok + row];
+          const float l = wp.lse[static_cast<int64_t>(w.g * p.G + c % p.G) * p.n_tok + row];
           if ((!wp.counted || wp.counted[row]) && l != -INFINITY) nl = -l * 1.44269504088896340736f;
         }
-        row_bits[r] = bits;
-        row_nlse[r] = nl;
+        row_bits[c] = bits;
+        row_nlse[c] = nl;
+        const uint32_t m = __ballot_sync(0xffffffffu, nl != -INFINITY);
+        if (lane == 0) live[c >> 5] = m;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->rows_ready[x]);
@@ -309,7 +355,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       };
       auto fetch = [&](int j, int pg, float& old, float& f) {
         const int at = (w.t0 + j) * 128 + r;
-        old = j < n && at < len ? acc[at] : 0.f;
+        old = !half && j < n && at < len ? acc[at] : 0.f;
         f = p.scale_log2;
         if (KV8) {
           f = 0.f;  // a page outside the pools reads as zeros
@@ -329,53 +375,76 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         tc_fence_after();
         const int d = at - w.ctx;  // >= 0: a drafted key
         const bool drafted = __any_sync(0xffffffffu, d >= 0);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+        const uint64_t ff = f2_pack(f, f);
+        const int chunks = (rows + 31) / 32, mid = HALVES == 1 ? chunks : (chunks + 1) / 2;
+        const int c_end = half ? chunks : mid;
 #pragma unroll 1
-        for (int c = 0; c < rows; c += 32) {
+        for (int c = half ? mid : 0; c < c_end; ++c) {
+          const int c0 = 32 * c;
           uint32_t sr[32];
-          tmem_ld32(s_tm + c, sr);
+          tmem_ld32(s_tm + c0, sr);
           tmem_ld_wait();
           reg_fence(sr);
-          if (!drafted) {
+          if (c0 + 32 > rows) {  // columns behind the rows may hold anything
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e >= rows) sr[e] = 0u;
+          }
+          if (drafted) {  // not every row sees the key
+            const bool in_reach = d < 64;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const float nl = row_nlse[c + e];
-              // a row that collects nothing may hold anything (it may lie behind the batch)
-              const float y = ex2_approx(fmaf(__uint_as_float(sr[e]), f, nl));
-              sum[e & 3] += nl == -INFINITY ? 0.f : y;
+              const bool seen = d < 0 || (in_reach && (row_bits[c0 + e] >> (d & 63) & 1u));
+              const float y = ex2_approx(fmaf(__uint_as_float(sr[e]), f, row_nlse[c0 + e]));
+              sum[e & 3] = f2_add(sum[e & 3], f2_pack(seen ? y : 0.f, 0.f));
             }
+          } else if (live[c] == 0xffffffffu) {
+            weights_add<true>(sr, ff, row_nlse + c0, sum);
           } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float nl = row_nlse[c + e];
-              const bool seen = nl != -INFINITY && (d < 0 || (d < 64 && (row_bits[c + e] >> d & 1u)));
-              const float y = ex2_approx(fmaf(__uint_as_float(sr[e]), f, nl));
-              sum[e & 3] += seen ? y : 0.f;
-            }
+            weights_add<false>(sr, ff, row_nlse + c0, sum);
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->s_empty[x]);
-        if (at < len) acc[at] = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        float s0, s1, s2, s3;
+        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+        f2_unpack(f2_add(sum[2], sum[3]), s2, s3);
+        float total = (s0 + s1) + (s2 + s3);
+        if (HALVES > 1 && chunks > 1) {
+          if (half) {
+            if (np > 0 && !(ok = warp_wait(&bars->part_empty[x], (np - 1) & 1, p.limit_ns, abort_flag, 943))) break;
+            *part = total;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->part_full[x]);
+          } else {
+            if (!(ok = warp_wait(&bars->part_full[x], np & 1, p.limit_ns, abort_flag, 944))) break;
+            total += *part;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->part_empty[x]);
+          }
+          ++np;
+        }
+        if (!half && at < len) acc[at] = old + total;
       }
       if (!ok || !w.next(p)) break;
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + 8 * HALVES) {
     // ================================================== e4m3: codes to bf16
     WeightWalk w;
     if (KV8 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
-      const int pt = threadIdx.x - 384;
+      const int pt = threadIdx.x - 128 * (1 + 2 * HALVES);
       const uint32_t raw_base = smem_u32(smem + SM::RAW);
       int item = 0;
       bool ok = true;
       do {
         for (int t = w.t0; t < w.t1 && ok; ++t, ++item) {
-          const int rs = item % CW_RAW, cs = item % ITEMS;
-          ok = warp_wait(&bars->raw_full[rs], (item / CW_RAW) & 1, p.limit_ns, abort_flag, 951) &&
+          const int rs = item % RAWS, cs = item % ITEMS;
+          ok = warp_wait(&bars->raw_full[rs], (item / RAWS) & 1, p.limit_ns, abort_flag, 951) &&
                (item < ITEMS || warp_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 952));
           if (!ok) break;
-          convert_tile(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, w.ctx + w.T - t * 128, pt);
+          convert_tile<CW_CONV>(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, w.ctx + w.T - t * 128, pt);
           fence_proxy_async_smem();
           __syncwarp();  // one arrival per warp: 256 of them would take longer than the conversion
           if (lane == 0) {
@@ -391,7 +460,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 2 * QR);
   }
 }
 

@@ -225,6 +225,14 @@ int launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap&
   return launched();
 }
 
+template <bool KV8, int QR>
+int launch_weights(const CUtensorMap& mq, const CUtensorMap& mk, const WeightParams& p, cudaStream_t st) {
+  constexpr uint32_t smem = WeightSmem<KV8, QR>::BYTES;
+  if (int rc = set_smem(cache_weights_kernel<KV8, QR>, smem)) return rc;
+  cache_weights_kernel<KV8, QR><<<static_cast<unsigned>(sm_count()), cw_threads(KV8), smem, st>>>(mq, mk, p);
+  return launched();
+}
+
 }  // namespace
 }  // namespace hs2
 
@@ -457,7 +465,8 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   if (!q || !lse || !acc) return HS2_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(acc) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return HS2_ERR_UNSUPPORTED;
   WeightParams p{};
-  p.t = tree_params(cache, draft, 128);
+  const int qr = draft->max_draft * (draft->Hq / cache->Hkv) <= 128 ? 128 : 256;  // rows of a pass
+  p.t = tree_params(cache, draft, qr);
   p.lse = lse;
   p.counted = counted;
   p.acc = acc;
@@ -468,15 +477,9 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   if (int rc = make_pool_map(&mk, cache, cache->k)) return rc;
   const Range range("hs2 cache_weights");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(sm_count());
-  if (cache->kv_dtype == HS2_KV_E4M3) {
-    if (int rc = set_smem(cache_weights_kernel<true>, WeightSmem<true>::BYTES)) return rc;
-    cache_weights_kernel<true><<<grid, tr_threads(true), WeightSmem<true>::BYTES, st>>>(mq, mk, p);
-  } else {
-    if (int rc = set_smem(cache_weights_kernel<false>, WeightSmem<false>::BYTES)) return rc;
-    cache_weights_kernel<false><<<grid, tr_threads(false), WeightSmem<false>::BYTES, st>>>(mq, mk, p);
-  }
-  return launched();
+  if (cache->kv_dtype == HS2_KV_E4M3)
+    return qr == 128 ? launch_weights<true, 128>(mq, mk, p, st) : launch_weights<true, 256>(mq, mk, p, st);
+  return qr == 128 ? launch_weights<false, 128>(mq, mk, p, st) : launch_weights<false, 256>(mq, mk, p, st);
 }
 
 }  // extern "C"

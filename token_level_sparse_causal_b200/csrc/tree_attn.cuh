@@ -303,10 +303,11 @@ __device__ __forceinline__ void e4m3x16_to_bf16(uint4 raw, uint4& a, uint4& b) {
 }
 
 // A raw tile of 128 rows of codes -> a bf16 tile in two 128-byte-swizzled
-// halves, by TR_CONV threads (pt); rows from `keys` on become zeros.  No
+// halves, by THREADS threads (pt); rows from `keys` on become zeros.  No
 // branch, so that a thread's rows overlap.
+template <int THREADS>
 __device__ __forceinline__ void convert_tile(uint32_t raw_tile, uint32_t tile, int keys, int pt) {
-  constexpr int STEP = TR_CONV / 8, ROWS = 128 / STEP;
+  constexpr int STEP = THREADS / 8, ROWS = 128 / STEP;
   const int c8 = pt & 7, row0 = pt >> 3;
   // lanes 0-3 and 4-7 of a row store their two chunks in opposite order, so
   // that a store touches every bank once
@@ -315,16 +316,20 @@ __device__ __forceinline__ void convert_tile(uint32_t raw_tile, uint32_t tile, i
   // a step keeps row & 7, so the chunks' places only move by whole rows
   const uint32_t dst1 = tile + sw128_chunk_offset(row0, 2 * c8 + (flip ? 1 : 0), 128);
   const uint32_t dst2 = tile + sw128_chunk_offset(row0, 2 * c8 + (flip ? 0 : 1), 128);
-  uint4 raw[ROWS];
+  constexpr int BATCH = 4;  // rows in registers
 #pragma unroll
-  for (int it = 0; it < ROWS; ++it) raw[it] = ld_shared_v4(src + it * STEP * 128);
+  for (int b0 = 0; b0 < ROWS; b0 += BATCH) {
+    uint4 raw[BATCH];
 #pragma unroll
-  for (int it = 0; it < ROWS; ++it) {
-    if (row0 + STEP * it >= keys) raw[it] = make_uint4(0, 0, 0, 0);
-    uint4 a, b;
-    e4m3x16_to_bf16(raw[it], a, b);
-    st_shared_v4(dst1 + it * STEP * 128, flip ? b : a);
-    st_shared_v4(dst2 + it * STEP * 128, flip ? a : b);
+    for (int it = 0; it < BATCH; ++it) raw[it] = ld_shared_v4(src + (b0 + it) * STEP * 128);
+#pragma unroll
+    for (int it = 0; it < BATCH; ++it) {
+      if (row0 + STEP * (b0 + it) >= keys) raw[it] = make_uint4(0, 0, 0, 0);
+      uint4 a, b;
+      e4m3x16_to_bf16(raw[it], a, b);
+      st_shared_v4(dst1 + (b0 + it) * STEP * 128, flip ? b : a);
+      st_shared_v4(dst2 + (b0 + it) * STEP * 128, flip ? a : b);
+    }
   }
 }
 
@@ -861,7 +866,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
             ok = warp_wait(&bars->raw_full[rs], (item / RAWS) & 1, p.limit_ns, abort_flag, 851) &&
                  (item < ITEMS || warp_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 852));
             if (!ok) break;
-            convert_tile(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, keys, pt);
+            convert_tile<TR_CONV>(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, keys, pt);
             fence_proxy_async_smem();
             __syncwarp();  // one arrival per warp: 256 of them would take longer than the conversion
             if (lane == 0) {
