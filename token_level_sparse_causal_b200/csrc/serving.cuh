@@ -387,9 +387,12 @@ int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const
   p.lse = lse;
   p.limit_ns = g_wait_limit_ns;
   p.flags = g_flags;
-  // at least one item per KV head for every pair of tiles any split of
-  // total_q tokens into n_seqs sequences can have
-  const int64_t items = s->total_q / (2 * p.rows_tok) + s->n_seqs;
+  // at least one item per KV head for every tile (pair) any split of total_q
+  // tokens into n_seqs sequences can have; single tiles while all of them run
+  // at once
+  const int64_t singles = s->total_q / p.rows_tok + s->n_seqs;
+  p.tiles = singles * s->Hkv <= sm_count() ? 1 : 2;
+  const int64_t items = p.tiles == 1 ? singles : s->total_q / (2 * p.rows_tok) + s->n_seqs;
   if (items * s->Hkv > (int64_t(1) << 31) - 1) return HS2_ERR_UNSUPPORTED;
   CUtensorMap mq, mk, mv;
   if (int rc = make_map(&mq, q, s->total_q, s->Hq, s->q_tok_stride, s->q_head_stride, p.G, p.rows_tok)) return rc;
@@ -398,10 +401,10 @@ int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const
     if (int rc = make_map(&mk, k, s->total_k, s->Hkv, s->kv_tok_stride, s->kv_head_stride, 1, 128)) return rc;
     if (int rc = make_map(&mv, v, s->total_k, s->Hkv, s->kv_tok_stride, s->kv_head_stride, 1, 128)) return rc;
   }
-  if (int rc = set_smem(varlen_attn_kernel, FL_SMEM_DENSE)) return rc;
+  if (int rc = set_smem(varlen_attn_kernel, VL_SMEM)) return rc;
   const Range range("hs2 varlen_attn");
-  varlen_attn_kernel<<<static_cast<unsigned>(items * s->Hkv), FL_THREADS, FL_SMEM_DENSE,
-                       static_cast<cudaStream_t>(stream)>>>(mq, mk, mv, p);
+  varlen_attn_kernel<<<static_cast<unsigned>(items * s->Hkv), FL_THREADS, VL_SMEM, static_cast<cudaStream_t>(stream)>>>(
+      mq, mk, mv, p);
   return launched();
 }
 

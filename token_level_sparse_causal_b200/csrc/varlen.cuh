@@ -9,14 +9,20 @@
 //            KV head, so a short prompt fills tiles (100 tokens at G = 8 are
 //            800 rows, 7 tiles, where tiles of one head would be 8 of them,
 //            each 100 / 128 full) and its K and V are loaded once for all
-//            heads; a CTA takes two consecutive tiles of one KV head;
-//   order    CTA -> (KV head, item), items longest first over all sequences:
+//            heads; an item is two consecutive tiles of one KV head, or one
+//            where few prompts leave SMs free (the chain of a single tile is
+//            shorter);
+//   order    index -> (KV head, item), items longest first over all sequences:
 //            item k lies at level p (the p-th tile pair of its sequence) with
 //            C(p + 1) <= k < C(p), C(p) = sum_b max(0, pairs_b - p), found by
-//            a binary search that one warp makes while the others set up.
-//            Only the sequences' total and their number size the grid, so the
-//            lengths stay on the device; the surplus CTAs (fewer than the
-//            sequences times the KV heads) come last and leave at once;
+//            a binary search of one warp. Only the sequences' total and their
+//            number size the grid, so the lengths stay on the device; surplus
+//            indexes (fewer than the sequences times the KV heads) come last;
+//   overlap  a CTA goes on to the next index that no CTA has started yet
+//            (cluster launch control: it cancels that CTA's launch and does its
+//            work), so the order stays the hardware's and the next item's
+//            queries and first keys load while the last one is still in its
+//            softmax and its epilogue;
 //   edges    keys behind a sequence's end are other sequences' or padding: a
 //            score there is replaced by -inf (whatever it was) and the V rows
 //            are zeroed in shared memory by an otherwise idle warp before
@@ -32,6 +38,7 @@ namespace hs2 {
 
 struct VarlenParams {
   int B, total_q, total_k, Hq, Hkv, G, rows_tok;
+  int tiles;  // of an item: 2, or 1 where that still leaves SMs free
   const int32_t *cu_q, *cu_k;
   float scale_log2;
   __nv_bfloat16* o;
@@ -41,49 +48,88 @@ struct VarlenParams {
   uint32_t flags;
 };
 
+// What the other roles need to know of an item; nq < 0: there is none left.
+struct VarlenItem {
+  int g, tok0;         // KV head, first token of its tiles
+  int q0, nq, k0, nk;  // the sequence's rows
+};
+
+constexpr int VL_ITEMS = 2;    // items known ahead
+constexpr int VL_READERS = 11;  // arrivals that give an item's slot back: 8 softmax warps, loads, products, warp 2
+
 struct VarlenBars {
-  uint64_t q_full;
+  uint64_t q_full, q_empty;
   uint64_t full_k[FL_STAGES], full_v[FL_STAGES], empty_k[FL_STAGES], empty_v[FL_STAGES];
-  uint64_t v_raw;  // the last V tile landed, its rows behind the sequence not yet zeroed
-  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t v_raw[FL_STAGES];  // a V tile landed whose rows behind the sequence are not yet zeroed
+  uint64_t s_full[2], p_ready[2], o_done[2], o_free;
+  uint64_t item_full[VL_ITEMS], item_empty[VL_ITEMS];
+  uint64_t loads_done;  // an item's loads are all under way
+  uint64_t next_full;   // an answer to "which index next" has come
   uint64_t fin;
   uint32_t tmem_slot;
   int abort;
-  int item_g, item_b, item_pair;  // item_g < 0: nothing to do
-  int q0, nq, k0, nk;
+  VarlenItem item[VL_ITEMS];
+  alignas(16) uint32_t next[4];
 };
-static_assert(sizeof(VarlenBars) <= 256, "barrier area");
-static_assert(4096 * 4 <= 2 * TILE_BYTES, "the item search borrows the first K/V stage");
+constexpr uint32_t VL_BAR_BYTES = 512;
+static_assert(sizeof(VarlenBars) <= VL_BAR_BYTES, "barrier area");
+constexpr uint32_t VL_PAIRS_OFF = FL_BAR_OFF + VL_BAR_BYTES;           // int [4096]: tile pairs of each sequence
+constexpr uint32_t VL_SMEM = VL_PAIRS_OFF + 4096 * 4 + 1024;           // + alignment slack
+static_assert(VL_SMEM <= 232448, "shared memory of one CTA");
 
-// One warp finds this CTA's item (see the order above); scratch holds B ints.
-__device__ __forceinline__ void varlen_find_item(const VarlenParams& p, int* scratch, VarlenBars* bars) {
+// An item's tiles: tile x reads key tiles 0 .. n_x - 1.
+struct VarlenTiles {
+  int nA, nB, n;
+  bool has_b;
+  int v_rows;  // rows of the last key tile that are keys
+  bool fix;    // it has others
+  __device__ __forceinline__ VarlenTiles(const VarlenItem& it, int R, int tiles) {
+    const int off = it.nk - it.nq;
+    has_b = tiles > 1 && it.tok0 + R < it.nq;
+    auto key_tiles = [&](int x) { return max(0, min(it.nq, it.tok0 + (x + 1) * R) + off + 127) >> 7; };
+    nA = key_tiles(0);
+    nB = has_b ? key_tiles(1) : 0;
+    n = max(nA, nB);
+    v_rows = it.nk - (n - 1) * 128;
+    fix = n > 0 && v_rows < 128;
+  }
+};
+
+// One warp counts the tile pairs of each sequence; returns their sum (0 where
+// an entry of cu_q or cu_k is bad) and the most of one sequence.
+__device__ __forceinline__ unsigned varlen_count(const VarlenParams& p, int* pairs, int& most) {
   const int lane = threadIdx.x & 31;
-  const int per = 2 * p.rows_tok;
+  const int per = p.tiles * p.rows_tok;
   bool ok = true;
-  int most = 0;
-  int64_t sum = 0;
+  most = 0;
+  unsigned sum = 0;  // <= total_q / per + B
   for (int b = lane; b < p.B; b += 32) {
     const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
     ok &= q0 >= 0 && q0 <= q1 && q1 <= p.total_q && k0 >= 0 && k0 <= k1 && k1 <= p.total_k;
     const int n = ok ? (q1 - q0 + per - 1) / per : 0;
-    scratch[b] = n;
+    pairs[b] = n;
     most = max(most, n);
-    sum += n;
+    sum += static_cast<unsigned>(n);
   }
-  ok = __all_sync(0xffffffffu, ok);
   most = __reduce_max_sync(0xffffffffu, most);
-  const unsigned total = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(sum));  // <= total_q / per + B
-  const int g = ok && total > 0 ? static_cast<int>(blockIdx.x / total) : p.Hkv;
-  if (!ok && lane == 0 && blockIdx.x == 0) report(HS2_ERR_INDEX, 701);
-  if (g >= p.Hkv) {
-    if (lane == 0) bars->item_g = -1;
-    return;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (!__all_sync(0xffffffffu, ok)) {
+    if (lane == 0 && blockIdx.x == 0) report(HS2_ERR_INDEX, 701);
+    return 0;
   }
-  const unsigned k = blockIdx.x % total;
-  __syncwarp();
+  return sum;
+}
+
+// One warp finds the item of index `index` (see the order above); each lane
+// reads only the counts that it wrote itself.  False: there is no such item.
+__device__ __forceinline__ bool varlen_find(const VarlenParams& p, const int* pairs, unsigned total, int most,
+                                            unsigned index, VarlenItem* item) {
+  const int lane = threadIdx.x & 31, per = p.tiles * p.rows_tok;
+  if (total == 0 || index / total >= static_cast<unsigned>(p.Hkv)) return false;
+  const unsigned g = index / total, k = index - g * total;
   auto at_least = [&](int level) {  // C(level)
     unsigned c = 0;
-    for (int b = lane; b < p.B; b += 32) c += static_cast<unsigned>(max(0, scratch[b] - level));
+    for (int b = lane; b < p.B; b += 32) c += static_cast<unsigned>(max(0, pairs[b] - level));
     return __reduce_add_sync(0xffffffffu, c);
   };
   int lo = 0, hi = most;  // C(lo) > k >= C(hi)
@@ -101,22 +147,45 @@ __device__ __forceinline__ void varlen_find_item(const VarlenParams& p, int* scr
   unsigned r = k - c_hi;  // rank among the sequences with more than lo pairs
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    const unsigned m = __ballot_sync(0xffffffffu, b < p.B && scratch[b] > lo);
+    const unsigned m = __ballot_sync(0xffffffffu, b < p.B && pairs[b] > lo);
     const unsigned c = __popc(m);
     if (r < c) {
       if ((m >> lane & 1u) && __popc(m & ((1u << lane) - 1u)) == static_cast<int>(r)) {
-        bars->item_g = g;
-        bars->item_b = b;
-        bars->item_pair = lo;
-        bars->q0 = p.cu_q[b];
-        bars->nq = p.cu_q[b + 1] - p.cu_q[b];
-        bars->k0 = p.cu_k[b];
-        bars->nk = p.cu_k[b + 1] - p.cu_k[b];
+        const int q0 = p.cu_q[b], k0 = p.cu_k[b];
+        *item = VarlenItem{static_cast<int>(g), lo * per, q0, p.cu_q[b + 1] - q0, k0, p.cu_k[b + 1] - k0};
       }
-      return;
+      break;
     }
     r -= c;
   }
+  __syncwarp();
+  return true;
+}
+
+// Asks for the index of a CTA of this grid that has not been launched yet, whose
+// launch is then cancelled; the answer (16 bytes) completes on `bar`.
+__device__ __forceinline__ void ask_next(uint32_t* answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The answer's index, or -1: no CTA is left to be launched.
+__device__ __forceinline__ int next_index(const uint32_t* answer) {
+  int index;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 x;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.b32 x, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 x, a;\n\t"
+      "mov.b32 %0, x;\n\t}"
+      : "=r"(index)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return index;
 }
 
 __global__ void __launch_bounds__(FL_THREADS, 1)
@@ -129,21 +198,30 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
   const uint32_t kv_base = smem_u32(smem + FL_KV_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &bars->abort;
+  const int R = p.rows_tok;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < FL_STAGES; ++s) {
       mbar_init(&bars->full_k[s], 1);
       mbar_init(&bars->full_v[s], 1);
       mbar_init(&bars->empty_k[s], 1);
       mbar_init(&bars->empty_v[s], 1);
+      mbar_init(&bars->v_raw[s], 1);
     }
-    mbar_init(&bars->v_raw, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
       mbar_init(&bars->p_ready[x], 4);
       mbar_init(&bars->o_done[x], 1);
     }
+    mbar_init(&bars->o_free, 8);
+    for (int s = 0; s < VL_ITEMS; ++s) {
+      mbar_init(&bars->item_full[s], 1);
+      mbar_init(&bars->item_empty[s], VL_READERS);
+    }
+    mbar_init(&bars->loads_done, 1);
+    mbar_init(&bars->next_full, 1);
     mbar_init(&bars->fin, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -155,180 +233,70 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
     tmem_alloc(&bars->tmem_slot, 512);
     tmem_relinquish();
   }
-  if (warp == 2) {
-    varlen_find_item(p, reinterpret_cast<int*>(smem + FL_KV_OFF), bars);
-    fence_proxy_async_smem();  // TMA writes the borrowed stage after the barrier
-  }
+  int most = 0;
+  unsigned total = 0;
+  int* pairs = reinterpret_cast<int*>(smem + VL_PAIRS_OFF);
+  if (warp == 3) total = varlen_count(p, pairs, most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
 
-  // ---- this CTA's two tiles (B may be absent); tile x reads key tiles 0 .. n_x - 1
-  const int g = bars->item_g;
-  const bool work = g >= 0;
-  const int R = p.rows_tok;
-  const int nq = bars->nq, nk = bars->nk, q0 = bars->q0, k0 = bars->k0;
-  const int tok0 = work ? bars->item_pair * 2 * R : 0;
-  const int off = nk - nq;
-  const bool has_b = work && tok0 + R < nq;
-  auto key_tiles = [&](int x) {
-    const int last = min(nq, tok0 + (x + 1) * R) - 1;
-    return max(0, last + off + 1 + 127) >> 7;
+  // the it-th item of this CTA, for a reader (a warp or one thread of it);
+  // false: there is none, or a wait ran out
+  auto item_of = [&](int it, VarlenItem& item) {
+    const int s = it % VL_ITEMS;
+    if (!mbar_wait(&bars->item_full[s], (it / VL_ITEMS) & 1, p.limit_ns, abort_flag, 702)) return false;
+    item = bars->item[s];
+    return item.nq >= 0;
   };
-  const int nA = work ? key_tiles(0) : 0;
-  const int nB = has_b ? key_tiles(1) : 0;
-  const int n = max(nA, nB);
-  const int v_rows = nk - (n - 1) * 128;  // rows of the last tile that are keys
-  const bool fix = n > 0 && v_rows < 128;
 
-  if (warp == 0) {
-    // =========================================================== TMA loads
-    if (lane == 0 && !(p.flags & FLAG_SKIP_LOADS) && n > 0) {
-      const int nqt = has_b ? 2 : 1;
-      const uint32_t half = static_cast<uint32_t>(R * p.G) * 128u;
-      mbar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(nqt) * 2u * half);
-      for (int x = 0; x < nqt; ++x) {
-        uint8_t* qd = smem + FL_Q_OFF + x * TILE_BYTES;
-        tma_load_3d(qd, &tmQ, &bars->q_full, 0, g * p.G, q0 + tok0 + x * R);
-        tma_load_3d(qd + HALF_BYTES, &tmQ, &bars->q_full, 64, g * p.G, q0 + tok0 + x * R);
-      }
-      int last = -1;
-      for (int j = 0; j < n; ++j) {
-        const int s = j % FL_STAGES;
-        const uint32_t par = ((j / FL_STAGES) - 1) & 1;
-        if (j >= FL_STAGES && !mbar_wait(&bars->empty_k[s], par, p.limit_ns, abort_flag, 711)) break;
-        uint8_t* kd = smem + FL_KV_OFF + s * 2 * TILE_BYTES;
-        mbar_arrive_expect_tx(&bars->full_k[s], TILE_BYTES);
-        tma_load_3d(kd, &tmK, &bars->full_k[s], 0, g, k0 + j * 128);
-        tma_load_3d(kd + HALF_BYTES, &tmK, &bars->full_k[s], 64, g, k0 + j * 128);
-        if (j >= FL_STAGES && !mbar_wait(&bars->empty_v[s], par, p.limit_ns, abort_flag, 712)) {
-          wait_done(&bars->full_k[s], (j / FL_STAGES) & 1, p.limit_ns, 713);
-          break;
-        }
-        // a last tile to be mended reaches full_v through warp 2
-        uint64_t* vbar = fix && j == n - 1 ? &bars->v_raw : &bars->full_v[s];
-        mbar_arrive_expect_tx(vbar, TILE_BYTES);
-        tma_load_3d(kd + TILE_BYTES, &tmV, vbar, 0, g, k0 + j * 128);
-        tma_load_3d(kd + TILE_BYTES + HALF_BYTES, &tmV, vbar, 64, g, k0 + j * 128);
-        last = j;
-      }
-      // never leave a TMA write in flight into memory the CTA gives back
-      for (int u = max(0, last - FL_STAGES + 1); u <= last; ++u) {
-        const int s = u % FL_STAGES;
-        wait_done(&bars->full_k[s], (u / FL_STAGES) & 1, p.limit_ns, 714);
-        if (fix && u == n - 1)
-          wait_done(&bars->v_raw, 0, p.limit_ns, 715);
-        else
-          wait_done(&bars->full_v[s], (u / FL_STAGES) & 1, p.limit_ns, 715);
-      }
-      wait_done(&bars->q_full, 0, p.limit_ns, 716);
-    }
-  } else if (warp == 1) {
-    // ========================================================== MMA issue
-    if (lane == 0 && n > 0) {
-      const int nx[2] = {nA, nB};
-      auto issue_s = [&](int x, int j) {
-        const uint32_t kb = kv_base + (j % FL_STAGES) * 2 * TILE_BYTES;
-        const uint32_t qb = q_base + x * TILE_BYTES;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-          umma_ss(tmem + x * 128, sdesc_sw128(qb + koff, 16, 1024), sdesc_sw128(kb + koff, 16, 1024), IDESC_S,
-                  kk > 0 ? 1u : 0u);
-        }
-        umma_commit(&bars->s_full[x]);
-      };
-      auto issue_pv = [&](int x, int j) {
-        const uint32_t vb = kv_base + (j % FL_STAGES) * 2 * TILE_BYTES + TILE_BYTES;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 2048, HALF_BYTES, 1024),
-                  IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-        if (j == nx[x] - 1) umma_commit(&bars->o_done[x]);
-      };
-      bool ok = mbar_wait(&bars->q_full, 0, p.limit_ns, abort_flag, 721);
-      if (ok) ok = mbar_wait(&bars->full_k[0], 0, p.limit_ns, abort_flag, 722);
-      if (ok) {
-        tc_fence_after();
-        for (int x = 0; x < 2; ++x)
-          if (nx[x] > 0) issue_s(x, 0);
-        umma_commit(&bars->empty_k[0]);
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        const int s = j % FL_STAGES;
-        if (!mbar_wait(&bars->full_v[s], (j / FL_STAGES) & 1, p.limit_ns, abort_flag, 723)) break;
-        if (j + 1 < n &&
-            !mbar_wait(&bars->full_k[(j + 1) % FL_STAGES], ((j + 1) / FL_STAGES) & 1, p.limit_ns, abort_flag, 724))
-          break;
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (j >= nx[x]) continue;
-          if (!mbar_wait(&bars->p_ready[x], j & 1, p.limit_ns, abort_flag, 726)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          issue_pv(x, j);
-          if (j + 1 < nx[x]) issue_s(x, j + 1);
-        }
-        if (ok) {
-          umma_commit(&bars->empty_v[s]);
-          if (j + 1 < n) umma_commit(&bars->empty_k[(j + 1) % FL_STAGES]);
-        }
-      }
-      umma_commit(&bars->fin);
-      wait_done(&bars->fin, 0, p.limit_ns, 727);
-    }
-  } else if (warp == 2) {
-    // ==================================== V rows behind the sequence's end
-    if (fix && !(p.flags & FLAG_SKIP_LOADS)) {
-      const int s = (n - 1) % FL_STAGES;
-      if (warp_wait(&bars->v_raw, 0, p.limit_ns, abort_flag, 731)) {
-        zero_rows(kv_base + s * 2 * TILE_BYTES + TILE_BYTES, v_rows, lane, 32);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->full_v[s]);
-      }
-    }
-  } else if (warp >= 4 && work) {
+  // registers move to the softmax warpgroups: 2 x 192 + 120 = 3 x 168
+  if (warp >= 4) {
+    reg_acquire<192>();
     // ============================================ softmax / rescale / epilogue
     const int x = (warp >= 8) ? 1 : 0;
-    const int nX = x ? nB : nA;
     const int r = threadIdx.x - 128 - 128 * x;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + x * 128;
     const uint32_t o_tm = tmem + lane_off + 256 + x * 128;
-    const int first = tok0 + x * R;
-    const int i_row = first + r / p.G;      // the row's query within its sequence
-    const int h = g * p.G + r % p.G;
-    const int limit = i_row + off;          // its last visible key
-    RowState st;
+    const int tok_r = r / p.G, head_r = r % p.G;
+    int ns = 0, no = 0;  // waits taken on s_full[x] and o_done[x]
+    VarlenItem item;
     bool ok = true;
-    for (int j = 0; j < nX; ++j) {
-      if (!warp_wait(&bars->s_full[x], j & 1, p.limit_ns, abort_flag, 741)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t sr[4][32];
-      load_scores(s_tm, sr);
-      if (j * 128 + 127 > first + off) mask_after(sr, limit - j * 128);
-      float alpha;
-      const bool resc = softmax_tile(s_tm, sr, p.scale_log2, st, alpha);
-      // P V(j - 1) completed before S(j): s_full's commit covers it
-      if (j > 0 && __any_sync(0xffffffffu, resc)) rescale_row(o_tm, alpha);
-      tmem_st_wait();
-      tc_fence_before();
+    for (int it = 0; ok && __all_sync(0xffffffffu, item_of(it, item)); ++it) {
+      const VarlenTiles t(item, R, p.tiles);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_ready[x]);
-    }
-    // ---- epilogue; a tile without a visible key writes zeros
-    const bool row_live = (x == 0 || has_b) && r < R * p.G && i_row < nq;
-    if (ok && (nX == 0 || warp_wait(&bars->o_done[x], 0, p.limit_ns, abort_flag, 742))) {
+      if (lane == 0) mbar_arrive(&bars->item_empty[it % VL_ITEMS]);
+      const int nX = x ? t.nB : t.nA;
+      const int first = item.tok0 + x * R, off = item.nk - item.nq;
+      const int i_row = first + tok_r;        // the row's query within its sequence
+      const int h = item.g * p.G + head_r;
+      const int limit = i_row + off;          // its last visible key
+      RowState st;
+      for (int j = 0; j < nX; ++j) {
+        if (!(ok = warp_wait(&bars->s_full[x], ns++ & 1, p.limit_ns, abort_flag, 741))) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
+        load_scores(s_tm, sr);
+        if (j * 128 + 127 > first + off) mask_after(sr, limit - j * 128);
+        float alpha;
+        const bool resc = softmax_tile(s_tm, sr, p.scale_log2, st, alpha);
+        // P V(j - 1) completed before S(j): s_full's commit covers it
+        if (j > 0 && __any_sync(0xffffffffu, resc)) rescale_row(o_tm, alpha);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_ready[x]);
+      }
+      // ---- epilogue; a tile without a visible key writes zeros
+      if (ok && nX > 0) ok = warp_wait(&bars->o_done[x], no++ & 1, p.limit_ns, abort_flag, 742);
+      if (!ok) break;
+      const bool row_live = (x == 0 || t.has_b) && r < R * p.G && i_row < item.nq;
       tc_fence_after();
       const float inv = st.l == 0.f ? 0.f : 1.f / st.l;
       __nv_bfloat16* orow =
-          p.o + static_cast<int64_t>(q0 + i_row) * p.o_tok + static_cast<int64_t>(h) * p.o_head;
+          p.o + static_cast<int64_t>(item.q0 + i_row) * p.o_tok + static_cast<int64_t>(h) * p.o_head;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t orr[32];
@@ -339,6 +307,11 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) orr[e] = 0u;
+        }
+        if (c == 3) {  // O is in registers: the next item's products may begin
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->o_free);
         }
         uint32_t pk[16];
 #pragma unroll
@@ -352,7 +325,185 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
         }
       }
       if (row_live && p.lse)
-        p.lse[static_cast<int64_t>(h) * p.total_q + q0 + i_row] = (st.m + log2f(st.l)) * 0.69314718055994530942f;
+        p.lse[static_cast<int64_t>(h) * p.total_q + item.q0 + i_row] =
+            (st.m + log2f(st.l)) * 0.69314718055994530942f;
+    }
+  } else {
+    reg_release<120>();
+    if (warp == 3) {
+      // ================================================================ items
+      unsigned index = blockIdx.x;
+      for (int it = 0;; ++it) {
+        const int s = it % VL_ITEMS;
+        if (it >= VL_ITEMS &&
+            !warp_wait(&bars->item_empty[s], (it / VL_ITEMS - 1) & 1, p.limit_ns, abort_flag, 703))
+          break;
+        const bool left = static_cast<int>(index) >= 0 && varlen_find(p, pairs, total, most, index, &bars->item[s]);
+        if (lane == 0) {
+          if (!left) bars->item[s].nq = -1;
+          mbar_arrive(&bars->item_full[s]);
+        }
+        if (!left) break;
+        // the next index once this item's loads are on their way: soon enough to
+        // load the next one behind them, late enough not to take an item that
+        // another CTA would start sooner
+        if (!warp_wait(&bars->loads_done, it & 1, p.limit_ns, abort_flag, 705)) break;
+        if (lane == 0) ask_next(bars->next, &bars->next_full);
+        if (!__all_sync(0xffffffffu, wait_done(&bars->next_full, it & 1, p.limit_ns, 704))) break;
+        index = static_cast<unsigned>(next_index(bars->next));
+        fence_proxy_async_smem();  // read before the next answer is written
+        __syncwarp();
+      }
+    } else if (warp == 0) {
+      // =========================================================== TMA loads
+      if (lane == 0 && !(p.flags & FLAG_SKIP_LOADS)) {
+        VarlenItem item;
+        int u = 0, nq_loads = 0;  // key tiles and query loads so far
+        uint32_t raw_used = 0, raw_uses = 0;  // stages last filled through v_raw, and how often (mod 2)
+        bool ok = true, k_alone = false;
+        for (int it = 0; ok && item_of(it, item); ++it) {
+          const VarlenTiles t(item, R, p.tiles);
+          if (t.n > 0) {
+            const int nqt = t.has_b ? 2 : 1;
+            const uint32_t half = static_cast<uint32_t>(R * p.G) * 128u;
+            if (nq_loads > 0 && !mbar_wait(&bars->q_empty, (nq_loads - 1) & 1, p.limit_ns, abort_flag, 711)) break;
+            ++nq_loads;
+            mbar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(nqt) * 2u * half);
+            for (int x = 0; x < nqt; ++x) {
+              uint8_t* qd = smem + FL_Q_OFF + x * TILE_BYTES;
+              tma_load_3d(qd, &tmQ, &bars->q_full, 0, item.g * p.G, item.q0 + item.tok0 + x * R);
+              tma_load_3d(qd + HALF_BYTES, &tmQ, &bars->q_full, 64, item.g * p.G, item.q0 + item.tok0 + x * R);
+            }
+            for (int j = 0; j < t.n; ++j, ++u) {
+              const int s = u % FL_STAGES;
+              const uint32_t par = ((u / FL_STAGES) - 1) & 1;
+              if (u >= FL_STAGES && !mbar_wait(&bars->empty_k[s], par, p.limit_ns, abort_flag, 712)) {
+                ok = false;
+                break;
+              }
+              uint8_t* kd = smem + FL_KV_OFF + s * 2 * TILE_BYTES;
+              mbar_arrive_expect_tx(&bars->full_k[s], TILE_BYTES);
+              tma_load_3d(kd, &tmK, &bars->full_k[s], 0, item.g, item.k0 + j * 128);
+              tma_load_3d(kd + HALF_BYTES, &tmK, &bars->full_k[s], 64, item.g, item.k0 + j * 128);
+              if (u >= FL_STAGES && !mbar_wait(&bars->empty_v[s], par, p.limit_ns, abort_flag, 713)) {
+                ok = false;
+                k_alone = true;  // K(u) in flight, V(u) not
+                break;
+              }
+              // a last tile to be mended reaches full_v through warp 2
+              const bool mend = t.fix && j == t.n - 1;
+              uint64_t* vbar = mend ? &bars->v_raw[s] : &bars->full_v[s];
+              raw_used = (raw_used & ~(1u << s)) | (mend ? 1u << s : 0u);
+              raw_uses ^= mend ? 1u << s : 0u;
+              mbar_arrive_expect_tx(vbar, TILE_BYTES);
+              tma_load_3d(kd + TILE_BYTES, &tmV, vbar, 0, item.g, item.k0 + j * 128);
+              tma_load_3d(kd + TILE_BYTES + HALF_BYTES, &tmV, vbar, 64, item.g, item.k0 + j * 128);
+            }
+          }
+          if (!ok) break;
+          mbar_arrive(&bars->loads_done);
+          mbar_arrive(&bars->item_empty[it % VL_ITEMS]);
+        }
+        // never leave a TMA write in flight into memory the CTA gives back
+        if (k_alone) wait_done(&bars->full_k[u % FL_STAGES], (u / FL_STAGES) & 1, p.limit_ns, 714);
+        for (int v = max(0, u - FL_STAGES); v < u; ++v) {
+          const int s = v % FL_STAGES;
+          if (!(k_alone && s == u % FL_STAGES)) wait_done(&bars->full_k[s], (v / FL_STAGES) & 1, p.limit_ns, 715);
+          if (raw_used >> s & 1u)
+            wait_done(&bars->v_raw[s], ~(raw_uses >> s) & 1u, p.limit_ns, 716);
+          else
+            wait_done(&bars->full_v[s], (v / FL_STAGES) & 1, p.limit_ns, 717);
+        }
+        if (nq_loads > 0) wait_done(&bars->q_full, (nq_loads - 1) & 1, p.limit_ns, 718);
+      }
+    } else if (warp == 1) {
+      // ========================================================== MMA issue
+      if (lane == 0) {
+        VarlenItem item;
+        int u = 0, nq_loads = 0, np[2] = {0, 0};
+        auto issue_s = [&](int x, int tile) {
+          const uint32_t kb = kv_base + (tile % FL_STAGES) * 2 * TILE_BYTES;
+          const uint32_t qb = q_base + x * TILE_BYTES;
+  #pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
+            umma_ss(tmem + x * 128, sdesc_sw128(qb + koff, 16, 1024), sdesc_sw128(kb + koff, 16, 1024), IDESC_S,
+                    kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bars->s_full[x]);
+        };
+        auto issue_pv = [&](int x, int tile, bool first, bool last) {
+          const uint32_t vb = kv_base + (tile % FL_STAGES) * 2 * TILE_BYTES + TILE_BYTES;
+  #pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 2048, HALF_BYTES, 1024),
+                    IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+          if (last) umma_commit(&bars->o_done[x]);
+        };
+        auto k_landed = [&](int tile) {
+          return mbar_wait(&bars->full_k[tile % FL_STAGES], (tile / FL_STAGES) & 1, p.limit_ns, abort_flag, 721);
+        };
+        bool ok = true;
+        for (int it = 0; ok && item_of(it, item); ++it) {
+          const VarlenTiles t(item, R, p.tiles);
+          const int n = t.n, nx[2] = {t.nA, t.nB};
+          if (n > 0) {
+            ok = mbar_wait(&bars->q_full, nq_loads++ & 1, p.limit_ns, abort_flag, 722) && k_landed(u);
+            if (!ok) break;
+            tc_fence_after();
+            for (int x = 0; x < 2; ++x)
+              if (nx[x] > 0) issue_s(x, u);
+            umma_commit(&bars->empty_k[u % FL_STAGES]);
+            if (n == 1) umma_commit(&bars->q_empty);
+          }
+          // the last item's O has been read (waited for at every item, as each
+          // has its phase)
+          if (it > 0 && !(ok = mbar_wait(&bars->o_free, (it - 1) & 1, p.limit_ns, abort_flag, 723))) break;
+          for (int j = 0; j < n && ok; ++j) {
+            const int tile = u + j, s = tile % FL_STAGES;
+            ok = mbar_wait(&bars->full_v[s], (tile / FL_STAGES) & 1, p.limit_ns, abort_flag, 724) &&
+                 (j + 1 >= n || k_landed(tile + 1));
+            for (int x = 0; x < 2 && ok; ++x) {
+              if (j >= nx[x]) continue;
+              if (!(ok = mbar_wait(&bars->p_ready[x], np[x]++ & 1, p.limit_ns, abort_flag, 725))) break;
+              tc_fence_after();
+              issue_pv(x, tile, j == 0, j == nx[x] - 1);
+              if (j + 1 < nx[x]) issue_s(x, tile + 1);
+            }
+            if (ok) {
+              umma_commit(&bars->empty_v[s]);
+              if (j + 1 < n) umma_commit(&bars->empty_k[(tile + 1) % FL_STAGES]);
+              if (j + 2 == n) umma_commit(&bars->q_empty);  // every score product is queued
+            }
+          }
+          u += n;
+          if (ok) mbar_arrive(&bars->item_empty[it % VL_ITEMS]);
+        }
+        umma_commit(&bars->fin);
+        wait_done(&bars->fin, 0, p.limit_ns, 726);
+      }
+    } else if (warp == 2) {
+      // ==================================== V rows behind the sequence's end
+      if (!(p.flags & FLAG_SKIP_LOADS)) {
+        VarlenItem item;
+        int u = 0;
+        uint32_t uses = 0;  // of each stage's v_raw, mod 2
+        for (int it = 0; __all_sync(0xffffffffu, item_of(it, item)); ++it) {
+          const VarlenTiles t(item, R, p.tiles);
+          u += t.n;
+          if (t.fix) {
+            const int s = (u - 1) % FL_STAGES;
+            if (!warp_wait(&bars->v_raw[s], uses >> s & 1u, p.limit_ns, abort_flag, 731)) break;
+            uses ^= 1u << s;
+            zero_rows(kv_base + s * 2 * TILE_BYTES + TILE_BYTES, t.v_rows, lane, 32);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->full_v[s]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->item_empty[it % VL_ITEMS]);
+        }
+      }
     }
   }
 
