@@ -315,6 +315,16 @@ def _strides(t: torch.Tensor) -> tuple:
     return (s[0] if n > 1 else H * head), head
 
 
+def _rows(t: torch.Tensor, n: int, H: int, what: str, device: int) -> tuple:
+    """Check of a bf16 [n][H][128] tensor with any token and head strides; returns them (see _strides)."""
+    s = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != (n, H, 128) or s[2] != 1 or t.get_device() != device:
+        _need_slow(t, torch.bfloat16, (n, H, 128), what, False, device)
+    if n > 1 and H > 1:
+        return s[0], s[1]
+    return _strides(t)
+
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -331,7 +341,7 @@ def _call(name: str, device: int, stream, *args) -> None:
         st = torch._C._cuda_getCurrentRawStream(device)
     else:
         st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    rc = getattr(lib(), name)(*args, st)
+    rc = getattr(_lib or lib(), name)(*args, st)
     if rc != HS2_OK:
         raise Hs2Error(rc, name)
 
@@ -367,24 +377,22 @@ def hs2_qk_norm_rope(cache: Hs2Cache, q, k, v, q_weight, k_weight, eps: float, i
     """q, q_out [n][Hq][128], k, v [n][Hkv][128] bf16 (any token and head strides), inv_freq float64 [rot / 2],
     positions and slots int32 [n] (slots None: rows 0 .. n - 1 of the pools; -1: no cache write)."""
     n, Hq, _ = q.shape
-    dev = cache.device
-    _need(q, torch.bfloat16, (n, Hq, 128), "q", False, dev)
-    _need(q_out, torch.bfloat16, (n, Hq, 128), "q_out", False, dev)
-    _need(k, torch.bfloat16, (n, cache.Hkv, 128), "k", False, dev)
-    _need(v, torch.bfloat16, (n, cache.Hkv, 128), "v", False, dev)
-    kv = _strides(k)
-    if _strides(v) != kv:
+    dev, Hkv, rot = cache.device, cache.Hkv, 2 * inv_freq.numel()
+    qs, outs = _rows(q, n, Hq, "q", dev), _rows(q_out, n, Hq, "q_out", dev)
+    kv = _rows(k, n, Hkv, "k", dev)
+    if _rows(v, n, Hkv, "v", dev) != kv:
         raise ValueError("v: must have k's strides")
     _need(q_weight, torch.bfloat16, (128,), "q_weight", True, dev)
     _need(k_weight, torch.bfloat16, (128,), "k_weight", True, dev)
-    _need(inv_freq, torch.float64, (inv_freq.numel(),), "inv_freq", True, dev)
+    _need(inv_freq, torch.float64, (rot // 2,), "inv_freq", True, dev)
     _need(positions, torch.int32, (n,), "positions", True, dev)
     _need(slots, torch.int32, (n,), "slots", True, dev)
     if slots is None and n > cache.n_pages * cache.page:
         raise ValueError(f"slots: {n} rows do not fit the pools' {cache.n_pages * cache.page} tokens")
-    r = Hs2Rope(n, Hq, 2 * inv_freq.numel(), int(interleaved), eps, 0, *_strides(q), *kv, *_strides(q_out))
-    _call("hs2_qk_norm_rope", dev, stream, ctypes.byref(cache), ctypes.byref(r), _addr(q), _addr(k), _addr(v),
-          _addr(q_weight), _addr(k_weight), _addr(inv_freq), _addr(positions), _addr(slots), _addr(q_out))
+    r = Hs2Rope(n, Hq, rot, 1 if interleaved else 0, eps, 0, qs[0], qs[1], kv[0], kv[1], outs[0], outs[1])
+    _call("hs2_qk_norm_rope", dev, stream, ctypes.byref(cache), ctypes.byref(r), q.data_ptr(), k.data_ptr(),
+          v.data_ptr(), _addr(q_weight), _addr(k_weight), inv_freq.data_ptr(), positions.data_ptr(), _addr(slots),
+          q_out.data_ptr())
 
 
 def make_varlen(q, k, n_seqs: int) -> Hs2Varlen:
@@ -398,13 +406,12 @@ def hs2_varlen_attn(shape: Hs2Varlen, q, k, v, cu_q, cu_k, o, lse=None, stream=N
     """q, o [total_q][Hq][128], k, v [total_k][Hkv][128]; cu_q, cu_k int32 [n_seqs + 1] (cu_k None: cu_q);
     lse fp32 [Hq][total_q] or None.  q and o, and k and v, have the strides make_varlen saw."""
     dev = q.get_device()
-    rows_q, st_q = (shape.total_q, shape.Hq, 128), (shape.q_tok_stride, shape.q_head_stride)
-    rows_k, st_k = (shape.total_k, shape.Hkv, 128), (shape.kv_tok_stride, shape.kv_head_stride)
-    for t, rows, st, name in ((q, rows_q, st_q, "q"), (o, rows_q, st_q, "o"), (k, rows_k, st_k, "k"),
-                              (v, rows_k, st_k, "v")):
-        _need(t, torch.bfloat16, rows, name, False, dev)
-        if _strides(t) != st:
-            raise ValueError(f"{name}: strides {_strides(t)}, expected {st}")
+    st_q, st_k = (shape.q_tok_stride, shape.q_head_stride), (shape.kv_tok_stride, shape.kv_head_stride)
+    for t, n, H, st, name in ((q, shape.total_q, shape.Hq, st_q, "q"), (o, shape.total_q, shape.Hq, st_q, "o"),
+                              (k, shape.total_k, shape.Hkv, st_k, "k"), (v, shape.total_k, shape.Hkv, st_k, "v")):
+        found = _rows(t, n, H, name, dev)
+        if found != st:
+            raise ValueError(f"{name}: strides {found}, expected {st}")
     _need(cu_q, torch.int32, (shape.n_seqs + 1,), "cu_q", True, dev)
     _need(cu_k, torch.int32, (shape.n_seqs + 1,), "cu_k", True, dev)
     _need(lse, torch.float32, (shape.Hq, shape.total_q), "lse", True, dev)
@@ -430,11 +437,10 @@ def _need_draft(cache: Hs2Cache, draft: Hs2Draft, q, o=None) -> None:
         raise ValueError(f"draft: {draft.n_seqs} sequences, the cache has {cache.n_seqs}")
     if draft.device != cache.device:
         raise ValueError(f"draft: on device {draft.device}, the cache is on {cache.device}")
+    st = (draft.q_tok_stride, draft.q_head_stride)
     for t, name in ((q, "q"), (o, "o")):
-        if t is not None:
-            _need(t, torch.bfloat16, (draft.n_tok, draft.Hq, 128), name, False, cache.device)
-            if _strides(t) != (draft.q_tok_stride, draft.q_head_stride):
-                raise ValueError(f"{name}: strides {_strides(t)} are not the draft's")
+        if t is not None and _rows(t, draft.n_tok, draft.Hq, name, cache.device) != st:
+            raise ValueError(f"{name}: strides {_strides(t)}, the draft's are {st}")
 
 
 def tree_attn_workspace_bytes(cache: Hs2Cache, draft: Hs2Draft) -> int:
