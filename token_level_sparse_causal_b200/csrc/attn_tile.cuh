@@ -93,24 +93,27 @@ __device__ __forceinline__ bool softmax_tile(uint32_t s_tm, const uint32_t (&sr)
 // The same for NQ quarters (32 columns each) of a tile from quarter q0 on, the
 // other columns' P set to zero; optionally (SCALED) with a K and a V scale per
 // key in shared memory ([128] each: scores are multiplied by the K scale, and P
-// times the V scale is what is rounded, the sum is of P), and with a mask of
-// visible columns (4 words).  The scores are read from tensor memory twice, a
-// quarter ahead of its use, so that a row takes 64 registers, not 128.
-template <int NQ, bool SCALED>
+// times the V scale is what is rounded, the sum is of P), and (MASKED) with the
+// visible columns in 4 words.  A whole tile's scores are read from tensor
+// memory twice, a quarter ahead of its use, so that a row takes 64 registers,
+// and in loops of two quarters: unrolled, with the mask's code among it, the
+// warps waited for instructions more than for anything else (3.5 of 13 cycles
+// an instruction).
+template <int NQ, bool SCALED, bool MASKED>
 __device__ __forceinline__ bool softmax_quarters(uint32_t s_tm, int q0, float sc, const float* kscale,
-                                                 const float* vscale, bool masked, const uint32_t (&vis)[4],
-                                                 RowState& st, float& alpha) {
+                                                 const float* vscale, const uint32_t (&vis)[4], RowState& st,
+                                                 float& alpha) {
+  static_assert(NQ == 1 || NQ == 2 || NQ == 4, "quarters");
   uint32_t buf[2][32];
-  auto issue = [&](int q) { tmem_ld32(s_tm + 32 * (q0 + q), buf[q & 1]); };
-  auto arrived = [&](int q) {
+  auto issue = [&](int q, uint32_t(&sr)[32]) { tmem_ld32(s_tm + 32 * q, sr); };
+  auto arrived = [&](uint32_t(&sr)[32]) {
     tmem_ld_wait();
-    reg_fence(buf[q & 1]);
+    reg_fence(sr);
   };
   // scores of quarter q as they enter the softmax
-  auto prepare = [&](int q) {
-    uint32_t(&sr)[32] = buf[q & 1];
+  auto prepare = [&](int q, uint32_t(&sr)[32]) {
     if (SCALED) {
-      const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(kscale + 32 * (q0 + q));
+      const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(kscale + 32 * q);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const ulonglong2 k2 = ks[e];  // broadcast
@@ -123,36 +126,37 @@ __device__ __forceinline__ bool softmax_quarters(uint32_t s_tm, int q0, float sc
         sr[4 * e + 3] = __float_as_uint(a3);
       }
     }
-    if (masked) {
-      const uint32_t w = NQ == 4 ? vis[q] : (q0 + q < 2 ? (q0 + q ? vis[1] : vis[0]) : (q0 + q == 2 ? vis[2] : vis[3]));
+    if (MASKED) {
+      const uint32_t w = q < 2 ? (q ? vis[1] : vis[0]) : (q == 2 ? vis[2] : vis[3]);
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         if (!(w >> e & 1u)) sr[e] = __float_as_uint(-INFINITY);
     }
   };
   float mx = -INFINITY;
-  issue(0);
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    arrived(q);
-    if (q + 1 < NQ) issue(q + 1);
-    prepare(q);
-    mx = fmaxf(mx, max32(buf[q & 1]));
-    if (NQ > 2 && q + 1 == NQ) issue(0);  // quarter 0 again; NQ <= 2: all are still in registers
+  issue(q0, buf[0]);
+#pragma unroll 1
+  for (int h = 0; h < (NQ == 4 ? 2 : 1); ++h) {
+    const int q = q0 + 2 * h;
+    arrived(buf[0]);
+    if (NQ > 1) issue(q + 1, buf[1]);
+    prepare(q, buf[0]);
+    mx = fmaxf(mx, max32(buf[0]));
+    if (NQ > 1) {
+      arrived(buf[1]);
+      if (NQ == 4) issue(h == 0 ? q + 2 : q0, buf[0]);  // at last quarter 0 again
+      prepare(q + 1, buf[1]);
+      mx = fmaxf(mx, max32(buf[1]));
+    }
   }
   const bool resc = update_max(mx * sc, st, alpha);
   const float mu = (st.m == -INFINITY) ? 0.f : st.m;
   const uint64_t sc2 = f2_pack(sc, sc), nmu2 = f2_pack(-mu, -mu);
   uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    if (NQ > 2) {
-      arrived(q);
-      if (q + 1 < NQ) issue(q + 1);
-      prepare(q);
-    }
-    const uint32_t(&sr)[32] = buf[q & 1];
-    const ulonglong2* vs = reinterpret_cast<const ulonglong2*>(vscale + 32 * (q0 + q));
+  // P of quarter q, over scores that this thread has read for the last time (a
+  // quarter on its way to registers lies behind them)
+  auto weigh = [&](int q, const uint32_t(&sr)[32]) {
+    const ulonglong2* vs = reinterpret_cast<const ulonglong2*>(vscale + 32 * q);
     uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -164,9 +168,23 @@ __device__ __forceinline__ bool softmax_quarters(uint32_t s_tm, int q0, float sc
       f2_unpack(p2, e0, e1);
       pk[e] = pack_bf16x2(e0, e1);
     }
-    // over scores that this thread has read for the last time: quarter q + 1,
-    // on its way to registers, lies behind column 16 (q + 1)
-    tmem_st16(s_tm + (q0 + q) * 16, pk);
+    tmem_st16(s_tm + 16 * q, pk);
+  };
+#pragma unroll 1
+  for (int h = 0; h < (NQ == 4 ? 2 : 1); ++h) {
+    const int q = q0 + 2 * h;
+    if (NQ == 4) {
+      arrived(buf[0]);
+      issue(q + 1, buf[1]);
+      prepare(q, buf[0]);
+    }
+    weigh(q, buf[0]);
+    if (NQ == 4) {
+      arrived(buf[1]);
+      if (h == 0) issue(q + 2, buf[0]);
+      prepare(q + 1, buf[1]);
+    }
+    if (NQ > 1) weigh(q + 1, buf[1]);
   }
   if (NQ < 4) {
     uint32_t zero[16];

@@ -460,8 +460,11 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           float alpha;
           bool resc;
           if constexpr (KV8 || BLOCKS > 1) {
-            resc = softmax_quarters<RB / 32, KV8>(s_tm, block * (RB / 32), p.scale_log2, sc_s, sc_s + 128, edge, vis,
-                                                  st, alpha);
+            const int q0 = block * (RB / 32);
+            if (edge)
+              resc = softmax_quarters<RB / 32, KV8, true>(s_tm, q0, p.scale_log2, sc_s, sc_s + 128, vis, st, alpha);
+            else
+              resc = softmax_quarters<RB / 32, KV8, false>(s_tm, q0, p.scale_log2, sc_s, sc_s + 128, vis, st, alpha);
           } else {
             uint32_t sr[4][32];
             load_scores(s_tm, sr);
