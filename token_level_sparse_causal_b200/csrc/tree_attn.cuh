@@ -4,9 +4,10 @@
 //
 // Bound by memory: K and V are read once (512 B per key and KV head in bf16,
 // 264 B as e4m3 with scales), and at T * G <= 128 rows one pass over them
-// serves all rows.  So the design is about keeping loads in flight:
+// serves all rows.  So the design is about keeping loads in flight (bf16,
+// 4 x 32768 tokens of 64/8 heads: T = 1 93 us, 5.8 TB/s; T = 16 107 us, 5.0):
 //
-//   work     the unit is (sequence, KV head, tile of 128 / G tokens); all units'
+//   work     the unit is (sequence, KV head, tile of RB / G tokens); all units'
 //            key tiles (128 keys) are laid end to end and every CTA (one per
 //            SM, persistent) takes an equal stretch, whatever the lengths: one
 //            long context is spread over all SMs, many short ones are packed.
@@ -24,14 +25,17 @@
 //   few rows a tile's 128 rows are 4 blocks of 32 (2 of 64) copies of the unit's
 //            rows where those fit, and block k keeps only its share of the
 //            tile's keys (the rest of its P is zero): all warps share one row's
-//            exponentials, instead of one warp taking all of them (about 2000
-//            cycles a tile, 4500 with an e4m3 cache's scales). Each block is a
+//            exponentials, instead of one warp taking all of them (T = 1, e4m3
+//            cache of 4 x 32768 tokens 137 -> 111 us; bf16 64 short sequences
+//            37.4 -> 35.5 us, but 4 x 32768 91.9 -> 92.9 and one sequence of 2048
+//            13.7 -> 14.3, for the blocks' O to be added). Each block is a
 //            softmax of its own; the epilogue adds the blocks' O, each block a
 //            share of the columns;
 //   e4m3     codes arrive by TMA in a raw ring; eight warps turn them into bf16
 //            (exact; unlike f16 it leaves Q and P their whole range), another
 //            fetches the scales; the K scale multiplies the scores, the V
-//            scale multiplies P before its rounding;
+//            scale multiplies P before its rounding. Bound by that softmax and
+//            the conversion, not by memory: 2.1 TB/s at 128 rows, 2.5 at 8;
 //   edges    columns without a visible key become -inf whatever they hold, V
 //            rows behind the last key are zeroed before the product.
 #pragma once
@@ -47,7 +51,7 @@ constexpr int TR_MAX_RAW = 5;    // e4m3: raw tiles of 16 KB, at most
 constexpr int TR_OVERHEAD = 3;   // what a unit costs beside its key tiles, in tiles (see tree_split)
 constexpr int TR_SCALES = 8;     // e4m3: key tiles whose scales are held or on their way
 constexpr uint32_t RAW_BYTES = 128u * 128u;
-constexpr int TR_CONV = 256;     // e4m3: converting threads (128: 229 us where 256 take 188)
+constexpr int TR_CONV = 256;     // e4m3: converting threads (4 x 131072 tokens, T = 16: 386 us, 128 of them 470)
 __host__ __device__ constexpr int tr_threads(bool kv8) { return 384 + (kv8 ? TR_CONV : 0); }
 
 // What a call's kernels share: the unit geometry.
@@ -454,26 +458,16 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         }
         if (warp_live) {
           const int base = (w.t0 + j) * 128;
-          const bool edge = base + 128 > w.ctx;
+          const int q0 = block * (RB / 32);
+          const float* vs_s = KV8 ? sc_s + 128 : nullptr;
           uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-          if (edge) tree_visible(w.ctx, base, bits, vis);
           float alpha;
           bool resc;
-          if constexpr (KV8 || BLOCKS > 1) {
-            const int q0 = block * (RB / 32);
-            if (edge)
-              resc = softmax_quarters<RB / 32, KV8, true>(s_tm, q0, p.scale_log2, sc_s, sc_s + 128, vis, st, alpha);
-            else
-              resc = softmax_quarters<RB / 32, KV8, false>(s_tm, q0, p.scale_log2, sc_s, sc_s + 128, vis, st, alpha);
+          if (base + 128 > w.ctx) {
+            tree_visible(w.ctx, base, bits, vis);
+            resc = softmax_quarters<RB / 32, KV8, true>(s_tm, q0, p.scale_log2, sc_s, vs_s, vis, st, alpha);
           } else {
-            uint32_t sr[4][32];
-            load_scores(s_tm, sr);
-            if (edge) {
-#pragma unroll
-              for (int c = 0; c < 128; ++c)
-                if (!(vis[c >> 5] >> (c & 31) & 1u)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-            }
-            resc = softmax_tile(s_tm, sr, p.scale_log2, st, alpha);
+            resc = softmax_quarters<RB / 32, KV8, false>(s_tm, q0, p.scale_log2, sc_s, vs_s, vis, st, alpha);
           }
           // P V(j - 2) completed before S(j): s_full's commit covers it
           if (j >= 2 && __any_sync(0xffffffffu, resc)) rescale_row(o_tm + 128 * x, alpha);
