@@ -95,6 +95,16 @@ def test_matches_oracle(lens, Hkv, page, keep, recent, kv8):
     _check(x, d, keep, recent)
 
 
+@pytest.mark.parametrize("B,Hkv", [(2, 8), (5, 5), (10, 4), (9, 8), (10, 12)])
+def test_clusters_of_every_size(B, Hkv):
+    """16 to 120 rows get clusters of 6 down to 1 CTAs."""
+    rng = np.random.default_rng(B)
+    x = _case([2500] + [int(n) for n in rng.integers(100, 2500, B - 1)], Hkv, bool(B & 1), 32, seed=B, values="ties")
+    d = _run(x, 400, 33)
+    hs2.hs2_sync()
+    _check(x, d, 400, 33)
+
+
 @pytest.mark.parametrize("kv8", [False, True])
 def test_more_rows_than_sms(kv8):
     """Above one row an SM a CTA has fewer threads: 160 rows, every length from none to some hundreds."""
@@ -170,3 +180,16 @@ def test_other_stream_and_graph_replay():
     g.replay()
     hs2.hs2_sync()
     _check(y, d, 100, 16)
+
+
+def test_acc_out_not_wanted():
+    x = _case([500, 10], 2, True, 64, seed=9)
+    d = {n: None if x[n] is None else x[n].clone().to(DEV) for n in ("k", "v", "ks", "vs", "table", "acc", "lens")}
+    cache = hs2.make_cache(d["k"], d["v"], d["table"], 64, d["ks"], d["vs"])
+    idx = torch.empty(2, 2, 60, dtype=torch.int32, device=DEV)
+    new_len = torch.empty(2, dtype=torch.int32, device=DEV)
+    hs2.hs2_cache_evict(cache, d["lens"], d["acc"], 60, 8, idx, new_len)
+    hs2.hs2_sync()
+    assert torch.equal(d["acc"].cpu(), x["acc"]) and new_len.tolist() == [60, 10]
+    for g in range(2):
+        assert idx[0, g].tolist() == so.kept_positions(x["acc"][0, g].numpy(), 500, 60, 8)

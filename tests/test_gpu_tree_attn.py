@@ -180,6 +180,45 @@ def test_rows_outside_the_sequences_are_left_alone():
         assert (o[edge] == 5).all() and (lse[:, edge] == 5).all()
 
 
+def test_without_lse_and_an_e4m3_cache_with_strides():
+    c = Paged([300, 41], [3, 5], 8, 2, True, 64, True, seed=16).device(DEV)
+    both = torch.zeros(c.k.shape[0], 4, 144, dtype=torch.uint8, device=DEV)   # codes of K and V side by side, padded
+    both[:, :2, :128], both[:, 2:, :128] = c.d["k"], c.d["v"]
+    cache = hs2.make_cache(both[:, :2, :128], both[:, 2:, :128], c.d["table"], 64, c.d["ks"], c.d["vs"])
+    o = torch.full_like(c.d["q"], 5.0)
+    hs2.hs2_tree_attn(cache, c.draft, c.d["q"], o, None, c.ws)
+    hs2.hs2_sync()
+    ref, rl, spread = c.oracle()
+    check_o(f64(o), ref, spread)
+    acc = torch.zeros((2, 2, c.max_pages * 64), device=DEV)
+    hs2.hs2_cache_weights(cache, c.draft, c.d["q"], torch.from_numpy(rl).float().to(DEV), None, acc)
+    hs2.hs2_sync()
+    assert torch.allclose(acc.sum(-1).double().cpu(), torch.tensor([[12.0, 12.0], [20.0, 20.0]], dtype=torch.float64),
+                          rtol=3e-4)                                   # every row of a group sums to one
+
+
+def test_more_drafts_than_said_are_reported():
+    c = Paged([130, 61], [3, 5], 8, 2, False, 64, True, seed=17).device(DEV)
+    ref, rl, spread = c.oracle()
+    c.draft = hs2.make_draft(c.d["q"], c.d["cu"], c.d["ctx"], c.d["mask"], 4)
+    o, lse, gb = _attend(c)
+    with pytest.raises(hs2.Hs2Error) as e:
+        hs2.hs2_sync()
+    assert e.value.code == hs2.HS2_ERR_INDEX
+    check_o(f64(o)[:3], ref[:3], spread[:3])
+    assert (o[3:] == 5).all()
+
+
+def test_sequences_that_share_pages():
+    """A common prefix lies in the cache once: two sequences name its pages."""
+    c = Paged([256, 256], [2, 3], 8, 2, False, 64, True, seed=18)
+    c.table[1, :4] = c.table[0, :4]
+    c.device(DEV)
+    o, lse, gb = _attend(c)
+    rl = _check(c, o, lse, gb)
+    _weights(c, rl)
+
+
 def test_bad_sequences_and_pages_are_reported():
     c = Paged([130, 61, 40], [3, 5, 2], 8, 2, False, 64, True, seed=10).device(DEV)
     ref, rl, spread = c.oracle()

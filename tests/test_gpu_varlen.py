@@ -130,6 +130,28 @@ def test_strided_views_of_one_projection():
     assert (o_all[:, Hq:] == 5).all()
 
 
+def test_without_lse():
+    cu = _cu([40, 200])
+    q, k, v = _inputs(cu, cu, 4, 2, seed=11)
+    o, lse, gb = _run(q, k, v, cu, None, with_lse=False)
+    o2, _, _ = _run(q, k, v, cu, None)
+    hs2.hs2_sync()
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and (lse == 5).all()
+    assert all(H.guards_intact(b) for b in gb)
+
+
+def test_single_and_paired_tiles_agree():
+    """The same prompt alone (single tiles, as SMs are free) and among many (pairs): bit for bit the same."""
+    rng = np.random.default_rng(12)
+    lens = [500] + [int(x) for x in rng.integers(100, 400, 60)]
+    cu = _cu(lens)
+    q, k, v = _inputs(cu, cu, 32, 8, seed=12)
+    o, lse, gb = _run(q, k, v, cu, None)
+    o1, lse1, _ = _run(q[:500].contiguous(), k[:500].contiguous(), v[:500].contiguous(), [0, 500], None)
+    hs2.hs2_sync()
+    assert torch.equal(o[:500].view(torch.int16), o1.view(torch.int16)) and torch.equal(lse[:, :500], lse1)
+
+
 def test_long_prompt_equals_kernel_1():
     """One sequence of a multiple of 64: the same attention as hs2_attn_fwd up to the weights' rounding."""
     L, Hq, Hkv = 8192, 8, 2
