@@ -367,8 +367,8 @@ typedef struct hs2_rope {
  * [0, n_pages * page) is reported by hs2_sync as HS2_ERR_INDEX and skipped.
  * The slots of one call must be distinct.
  *
- * q_weight, k_weight: bf16 [128], both NULL or both given.  inv_freq: double
- * [rot / 2].  positions: int32 [n].  slots: int32 [n] or NULL.  q_out may be
+ * q_weight, k_weight: bf16 [128], 16-byte aligned, both NULL or both given.
+ * inv_freq: double [rot / 2].  positions: int32 [n].  slots: int32 [n] or NULL.  q_out may be
  * q (same strides), and nothing else may overlap an input.  n = 0 does nothing.
  * page_table, n_seqs and max_pages of the cache are not read.  Device
  * pointers; asynchronous on `stream`.
@@ -406,7 +406,7 @@ typedef struct hs2_varlen {
  * to cu_q.  Entries that descend or leave [0, total] are reported by hs2_sync
  * as HS2_ERR_INDEX, and the call then writes nothing.  The values of a
  * sequence's own tokens have to be finite; tokens outside the sequences may
- * hold anything.  Asynchronous on `stream`.
+ * hold anything.  o must not overlap an input.  Asynchronous on `stream`.
  */
 int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const void* v, const int32_t* cu_q,
                     const int32_t* cu_k, void* o, float* lse, void* stream);
@@ -440,8 +440,8 @@ typedef struct hs2_draft {
  * lse fp32 [Hq][n_tok] (optional, natural log).  A row that sees nothing gets
  * zeros and -inf.  Values of tokens inside a sequence (committed or drafted)
  * have to be finite, those behind it in its last page may be anything.
- * Rows of q and o outside [cu_draft[0], cu_draft[n_seqs]) are left alone.
- * n_tok = 0 does nothing.
+ * Rows of o outside [cu_draft[0], cu_draft[n_seqs]) are left alone, those of q
+ * may hold anything.  o must not overlap an input.  n_tok = 0 does nothing.
  *
  * workspace: hs2_tree_attn_workspace(cache, draft) bytes, 16-byte aligned; it
  * holds no state between calls, but two calls in flight at once (two graphs
