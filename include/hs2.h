@@ -462,8 +462,9 @@ int hs2_tree_attn_workspace(const hs2_cache* cache, const hs2_draft* draft, size
  * [n_tok], rows with 0 are left out (drafted tokens that were not accepted);
  * NULL counts all.  Rows with lse = -inf collect nothing.  acc: fp32
  * [n_seqs][Hkv][acc_stride]; acc_stride a multiple of 4 and at least every
- * length.  Positions behind a sequence are not touched.  The sums are added in
- * a fixed order; two calls on one acc must not run at once.
+ * length: a longer sequence is reported as HS2_ERR_INDEX and left out.
+ * Positions behind a sequence are not touched.  The sums are added in a fixed
+ * order; two calls on one acc must not run at once.
  */
 int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void* q, const float* lse,
                       const uint8_t* counted, float* acc, int64_t acc_stride, void* stream);

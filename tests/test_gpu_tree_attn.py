@@ -252,6 +252,25 @@ def test_bad_sequences_and_pages_are_reported():
     _check(c, o, lse, gb)
 
 
+@pytest.mark.parametrize("kv8", [False, True])
+def test_an_acc_shorter_than_a_sequence_is_reported(kv8):
+    c = Paged([130, 61, 98], [3, 5, 2], 8, 2, kv8, 64, True, seed=19).device(DEV)
+    ref, rl, spread = c.oracle()
+    lse = torch.from_numpy(rl).float().to(DEV)
+    room = torch.full((3 * 2 * 100 + 256,), 7.0, device=DEV)  # 133 tokens of sequence 0 do not fit, 66 and 100 do
+    acc = room[:600].view(3, 2, 100)
+    acc.zero_()
+    hs2.hs2_cache_weights(c.cache, c.draft, c.d["q"], lse, None, acc)
+    with pytest.raises(hs2.Hs2Error) as e:
+        hs2.hs2_sync()
+    assert e.value.code == hs2.HS2_ERR_INDEX
+    assert (room[600:] == 7).all() and (acc[0] == 0).all()
+    full = torch.zeros((3, 2, c.max_pages * 64), device=DEV)
+    hs2.hs2_cache_weights(c.cache, c.draft, c.d["q"], lse, None, full)
+    hs2.hs2_sync()
+    assert torch.equal(acc[1:], full[1:, :, :100]) and (full[0, :, :133] > 0).all()
+
+
 def test_streams_graphs_and_repeats():
     c = Paged([900, 61, 400], [3, 5, 2], 16, 2, False, 64, True, seed=11).device(DEV)
     st = torch.cuda.Stream()

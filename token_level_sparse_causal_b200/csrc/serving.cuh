@@ -105,6 +105,7 @@ TreeParams tree_params(const hs2_cache* c, const hs2_draft* d, int rows) {
   p.page_log2 = log2_of(c->page);
   p.n_pages = c->n_pages;
   p.max_pages = c->max_pages;
+  p.max_len = static_cast<int64_t>(c->max_pages) * c->page;
   p.n_tok = d->n_tok;
   p.max_draft = d->max_draft;
   p.table = c->page_table;
@@ -474,6 +475,7 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   p.counted = counted;
   p.acc = acc;
   p.acc_stride = acc_stride;
+  p.t.max_len = std::min(p.t.max_len, acc_stride);
   CUtensorMap mq, mk;
   if (int rc = make_map(&mq, q, draft->n_tok, draft->Hq, draft->q_tok_stride, draft->q_head_stride, p.t.G, p.t.R))
     return rc;

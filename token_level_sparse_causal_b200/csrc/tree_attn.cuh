@@ -57,6 +57,7 @@ __host__ __device__ constexpr int tr_threads(bool kv8) { return 384 + (kv8 ? TR_
 // What a call's kernels share: the unit geometry.
 struct TreeParams {
   int B, Hq, Hkv, G, R, page_log2, n_pages, max_pages, n_tok, max_draft;
+  int64_t max_len;  // tokens of a sequence, drafted ones with them: what the table (and acc) can hold
   const int32_t *table, *cu, *ctx;
   const uint64_t* mask;
   float scale_log2;
@@ -111,8 +112,7 @@ struct TreeSmem {
 // A sequence's lengths; a bad entry counts as no drafted tokens.
 __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, int& row0, int& T, int& ctx) {
   const int64_t r0 = p.cu[b], t = static_cast<int64_t>(p.cu[b + 1]) - r0, c = p.ctx[b];
-  const bool ok = r0 >= 0 && t >= 0 && t <= p.max_draft && r0 + t <= p.n_tok && c >= 0 &&
-                  c + t <= (static_cast<int64_t>(p.max_pages) << p.page_log2);
+  const bool ok = r0 >= 0 && t >= 0 && t <= p.max_draft && r0 + t <= p.n_tok && c >= 0 && c + t <= p.max_len;
   row0 = ok ? static_cast<int>(r0) : 0;
   T = ok ? static_cast<int>(t) : 0;
   ctx = ok ? static_cast<int>(c) : 0;
