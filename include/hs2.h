@@ -483,7 +483,7 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
  *
  * acc fp32 [n_seqs][Hkv][acc_stride], finite values; acc_out the same layout,
  * may be acc itself or NULL (not wanted), but not overlap it otherwise.
- * new_len must not be seq_len.  0 <= recent <= keep, 1 <= keep <= 2^24.
+ * new_len must not overlap seq_len.  0 <= recent <= keep, 1 <= keep <= 2^24.
  * No page of the table may appear twice among the sequences' pages in use.
  * A length outside [0, max_pages * page] or above acc_stride, or a page
  * outside the pools, is reported by hs2_sync as HS2_ERR_INDEX; such a

@@ -180,6 +180,15 @@ def test_bad_evictions(lib, kw, code):
     assert evict_call(lib, cache(), **kw) == code
 
 
+def test_evictions_whose_outputs_overlap_inputs(lib):
+    far = P + (1 << 20)
+    assert evict_call(lib, cache(), lens=P, new=P, acc_out=far) == INV
+    assert evict_call(lib, cache(), lens=P + 4, new=P, acc_out=far) == INV
+    assert evict_call(lib, cache(), lens=P, new=P + 4, acc_out=far) == INV
+    assert evict_call(lib, cache(), acc=P + 1024, acc_out=P) == INV
+    assert evict_call(lib, cache(), acc=P, acc_out=P + 1024) == INV
+
+
 def test_python_checks_name_the_argument():
     k = torch.zeros(128, 2, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="page"):

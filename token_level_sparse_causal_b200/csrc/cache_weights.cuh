@@ -3,34 +3,40 @@
 //                   exp(q_rh . k_j / sqrt(d) - lse[h][r])   (0 where j is masked)
 //
 // As kernel (2) (importance.cuh) the keys lie on the MMA's M dimension: D =
-// K tile (128 keys x d) * Q^T (d x up to 256 query rows), so TMEM lane r holds
+// K tile (128 keys x d) * Q^T (d x up to CW_ROWS query rows), so TMEM lane r holds
 // key r against every row and the thread that owns it adds its row up in
 // registers, with no reduction between threads and no atomics: each position
 // is written by one thread, in a fixed order.
 //
 // K is read once (256 B a key and KV head, 132 B as e4m3).  Work is split as
 // in tree_attn.cuh, but by (sequence, KV head): a CTA takes an equal stretch of
-// all key tiles, and for more than QR rows walks its part of a sequence once
-// per QR rows (adding to what it wrote; the K tiles then come from L2).  Of a
+// all key tiles, and for more than CW_ROWS rows walks its part of a sequence
+// once per CW_ROWS rows (adding to what it wrote; the K tiles then come from
+// L2).  Of a
 // bf16 cache two pairs of epilogue warpgroups take the even and the odd tiles,
 // each warpgroup half of the columns (with one a tile 32 columns took 700
 // cycles of mostly waiting); the second hands its sums to the first through
 // shared memory.  An e4m3 cache leaves registers for one warpgroup a tile
-// beside the converting warps.  Bound by memory up to about 100 rows, then by
-// the exponentials: 16 a clock and SM on the MUFU unit, so where all 32 columns
-// of a chunk count six of its sixteen pairs take the degree-4 polynomial on the
-// FMA pipes instead (2.6e-6; the cubic that kernel (2) mixes in is exact only
-// to 7.5e-5).
+// beside the converting warps.  Bound by memory up to about 100 rows (bf16, 4 x
+// 32768 tokens of 64/8 heads: 8 rows 51 us, 5.4 TB/s; 128 rows 61 us, 4.5), then
+// by the exponentials (512 rows 191 us): 16 a clock and SM on the MUFU unit, so
+// where all 32 columns of a chunk count six of its sixteen pairs take the
+// degree-4 polynomial on the FMA pipes instead (2.6e-6; the cubic that kernel
+// (2) mixes in is exact only to 7.5e-5).
 //
 // e4m3: codes arrive by TMA in a raw ring and are turned into bf16 by eight
-// warps; the key's scale multiplies its row of scores.
+// warps; the key's scale multiplies its row of scores.  Bound by the conversion
+// at few rows (60 us, 2.4 TB/s), by the sums of the one warpgroup a tile at many
+// (128 rows 89 us, 512 rows 277).
 #pragma once
 
 #include "tree_attn.cuh"
 
 namespace hs2 {
 
-constexpr int CW_MAX_ITEMS = 5;  // K tiles in the ring, at most
+constexpr int CW_ROWS = 256;     // query rows of a pass; 128 of them: 222 us for 192 with 512 rows of a
+                                 // bf16 cache (above), 326 for 277 of an e4m3 one, 58 for 60 with 8 rows
+constexpr int CW_MAX_ITEMS = 4;  // K tiles in the ring, at most
 constexpr int CW_MAX_RAW = 5;    // e4m3: raw tiles, at most
 constexpr int CW_CONV = 256;     // e4m3: converting threads
 __host__ __device__ constexpr int cw_halves(bool kv8) { return kv8 ? 1 : 2; }  // epilogue warpgroups of a tile
@@ -60,10 +66,10 @@ struct WeightBars {
 };
 static_assert(sizeof(WeightBars) <= 512, "barrier area");
 
-// QR: query rows of a pass, 128 or 256.
-template <bool KV8, int QR>
+template <bool KV8>
 struct WeightSmem {
-  static constexpr int ITEMS = KV8 ? (QR == 256 ? 2 : 3) : (QR == 256 ? 4 : 5);
+  static constexpr int QR = CW_ROWS;
+  static constexpr int ITEMS = KV8 ? 2 : 4;
   static constexpr int RAWS = 5;
   static_assert(ITEMS <= CW_MAX_ITEMS && RAWS <= CW_MAX_RAW, "rings");
   static constexpr uint32_t QHALF = QR * 128u;
@@ -74,7 +80,7 @@ struct WeightSmem {
   static constexpr uint32_t BITS = BAR + 512u;                // uint64 [2][2][QR]: the drafted keys it sees
   static constexpr uint32_t NLSE = BITS + 2 * 2 * QR * 8u;    // float [2][2][QR]: -lse * log2(e), -inf: none
   static constexpr uint32_t LIVE = NLSE + 2 * 2 * QR * 4u;    // uint32 [2][2][QR / 32]: the columns that collect
-  static constexpr uint32_t PART = LIVE + 2 * 2 * QR / 8u;  // float [2][128]
+  static constexpr uint32_t PART = LIVE + 2 * 2 * QR / 8u;    // float [2][128]
   static constexpr uint32_t BYTES = PART + 1024u;
   static_assert(BYTES <= 232448u, "shared memory of one CTA");
 };
@@ -147,12 +153,12 @@ __device__ __forceinline__ void weights_add(const uint32_t (&sr)[32], uint64_t f
   }
 }
 
-template <bool KV8, int QR>
+template <bool KV8>
 __global__ void __launch_bounds__(cw_threads(KV8), 1)
     cache_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const WeightParams wp) {
-  using SM = WeightSmem<KV8, QR>;
-  constexpr int ITEMS = SM::ITEMS, RAWS = SM::RAWS, HALVES = cw_halves(KV8);
+  using SM = WeightSmem<KV8>;
+  constexpr int QR = SM::QR, ITEMS = SM::ITEMS, RAWS = SM::RAWS, HALVES = cw_halves(KV8);
   const TreeParams& p = wp.t;
   extern __shared__ __align__(1024) uint8_t weights_smem[];
   uint8_t* smem = weights_smem;

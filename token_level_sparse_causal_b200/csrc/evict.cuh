@@ -266,15 +266,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) cache_evict_kernel(co
   const int batch = step * EV_ROWS;
   const int ctid = rank * THREADS + tid;  // scalars of row ctid of a batch
   int old[EV_ROWS];  // old positions of the batch's rows, read a batch ahead
+  // (-1 for what is no position: weights that change under the call leave holes in the list)
+  auto listed = [&](int i) {
+    const int x = i < p.keep ? idx[i] : -1;
+    return x < n ? x : -1;
+  };
   auto olds_of = [&](int i0) {
 #pragma unroll
-    for (int e = 0; e < EV_ROWS; ++e) {
-      const int i = i0 + e * step + row0;
-      old[e] = i < p.keep ? idx[i] : -1;
-    }
+    for (int e = 0; e < EV_ROWS; ++e) old[e] = listed(i0 + e * step + row0);
   };
   olds_of(0);
-  auto scalar_of = [&](int i0) { return ctid < batch && i0 + ctid < p.keep ? idx[i0 + ctid] : -1; };
+  auto scalar_of = [&](int i0) { return ctid < batch ? listed(i0 + ctid) : -1; };
   int was_next = scalar_of(0);
   for (int i0 = 0; i0 < p.keep; i0 += batch) {
     uint4 data[EV_ROWS];

@@ -32,6 +32,11 @@ int log2_of(int page) {
   }
 }
 
+bool overlap(const void* a, const void* b, uint64_t bytes) {
+  const uint64_t x = reinterpret_cast<uint64_t>(a), y = reinterpret_cast<uint64_t>(b);
+  return x < y ? y - x < bytes : x - y < bytes;
+}
+
 // table: whether the call reads the page table.
 int check_cache(const hs2_cache* c, bool table) {
   if (!c || !c->k || !c->v) return HS2_ERR_INVALID_ARG;
@@ -226,11 +231,11 @@ int launch_tree(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap&
   return launched();
 }
 
-template <bool KV8, int QR>
+template <bool KV8>
 int launch_weights(const CUtensorMap& mq, const CUtensorMap& mk, const WeightParams& p, cudaStream_t st) {
-  constexpr uint32_t smem = WeightSmem<KV8, QR>::BYTES;
-  if (int rc = set_smem(cache_weights_kernel<KV8, QR>, smem)) return rc;
-  cache_weights_kernel<KV8, QR><<<static_cast<unsigned>(sm_count()), cw_threads(KV8), smem, st>>>(mq, mk, p);
+  constexpr uint32_t smem = WeightSmem<KV8>::BYTES;
+  if (int rc = set_smem(cache_weights_kernel<KV8>, smem)) return rc;
+  cache_weights_kernel<KV8><<<static_cast<unsigned>(sm_count()), cw_threads(KV8), smem, st>>>(mq, mk, p);
   return launched();
 }
 
@@ -306,13 +311,17 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   using namespace hs2;
   if (int rc = check_cache(cache, true)) return rc;
   if (!seq_len || !acc || !idx || !new_len) return HS2_ERR_INVALID_ARG;
-  if (keep < 1 || recent < 0 || recent > keep || new_len == seq_len) return HS2_ERR_INVALID_ARG;
+  if (keep < 1 || recent < 0 || recent > keep) return HS2_ERR_INVALID_ARG;
   if (acc_stride <= 0 || acc_stride % 4) return HS2_ERR_INVALID_ARG;
-  if (keep > (1 << 24)) return HS2_ERR_UNSUPPORTED;
+  if (keep > (1 << 24) || acc_stride > (int64_t(1) << 31)) return HS2_ERR_UNSUPPORTED;
   if (!aligned16(acc) || (acc_out && !aligned16(acc_out))) return HS2_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(seq_len) | reinterpret_cast<uintptr_t>(idx) |
        reinterpret_cast<uintptr_t>(new_len)) & 3u)
     return HS2_ERR_UNSUPPORTED;
+  // the CTAs of a row have to read the same lengths and weights, whichever rows are done
+  const uint64_t acc_bytes = static_cast<uint64_t>(acc_stride) * 4u * static_cast<uint64_t>(cache->n_seqs) * cache->Hkv;
+  if (overlap(seq_len, new_len, static_cast<uint64_t>(cache->n_seqs) * 4u)) return HS2_ERR_INVALID_ARG;
+  if (acc_out && acc_out != acc && overlap(acc, acc_out, acc_bytes)) return HS2_ERR_INVALID_ARG;
   EvictParams p{};
   const bool kv8 = cache->kv_dtype == HS2_KV_E4M3;
   p.Hkv = cache->Hkv;
@@ -469,8 +478,7 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   if (!q || !lse || !acc) return HS2_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(acc) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return HS2_ERR_UNSUPPORTED;
   WeightParams p{};
-  const int qr = draft->max_draft * (draft->Hq / cache->Hkv) <= 128 ? 128 : 256;  // rows of a pass
-  p.t = tree_params(cache, draft, qr);
+  p.t = tree_params(cache, draft, CW_ROWS);
   p.lse = lse;
   p.counted = counted;
   p.acc = acc;
@@ -482,9 +490,7 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   if (int rc = make_pool_map(&mk, cache, cache->k)) return rc;
   const Range range("hs2 cache_weights");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->kv_dtype == HS2_KV_E4M3)
-    return qr == 128 ? launch_weights<true, 128>(mq, mk, p, st) : launch_weights<true, 256>(mq, mk, p, st);
-  return qr == 128 ? launch_weights<false, 128>(mq, mk, p, st) : launch_weights<false, 256>(mq, mk, p, st);
+  return cache->kv_dtype == HS2_KV_E4M3 ? launch_weights<true>(mq, mk, p, st) : launch_weights<false>(mq, mk, p, st);
 }
 
 }  // extern "C"
