@@ -12,13 +12,14 @@
 // lane, so the norm and the row's amax are four shuffles and the partner
 // dimension of the half-split rotation lies rot / 16 lanes away; each half-warp
 // has the loads of four rows in flight while it works on four others.  32768
-// tokens of 64/8 heads: 208 us, 6.4 TB/s into a bf16 cache, 6.1 into e4m3.
+// tokens of 64/8 heads: 207 us, 6.5 TB/s into a bf16 cache, 6.2 into e4m3.
 //
 // A half-warp stays with one token, so its lane's eight sines and cosines and
 // the weights sit in registers for all of the token's heads: read from shared
 // memory for every row they made the shared-memory pipe the bound (32768 tokens
-// of 64/8 heads took 331 us).  Few tokens: a CTA per token,
-// its heads over all half-warps; many: a warp per token.  The angle in turns,
+// of 64/8 heads took 331 us).  Few tokens: a CTA per token, its heads over all
+// half-warps (512 tokens 8.2 us, a warp per token 12.3); many: a warp per token
+// (4096 tokens 36 us, a CTA per token 44).  The angle in turns,
 // t * inv_freq / (2 pi), is formed and reduced in 64 bits (at t = 2^20 an fp32
 // product would be off by 0.06 rad) once per token; sine and cosine of the
 // reduced turn are fp32.  Everything else is fp32 with one rounding at the store.

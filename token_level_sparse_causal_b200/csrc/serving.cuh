@@ -300,7 +300,8 @@ int hs2_qk_norm_rope(const hs2_cache* cache, const hs2_rope* rope, const void* q
   p.c_tok = cache->tok_stride;
   p.c_head = cache->head_stride;
   p.n_slots = static_cast<int64_t>(cache->n_pages) * cache->page;
-  // a CTA per token until that fills the GPU a few times over, then a warp per token
+  // a CTA per token until that fills the GPU a few times over, then a warp per
+  // token (norm_rope.cuh has both sides' times)
   const bool kv8 = cache->kv_dtype == HS2_KV_E4M3, pairs = rope->interleaved != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return p.n >= sm_count() * 16 ? launch_norm_rope<8>(p, kv8, pairs, st) : launch_norm_rope<1>(p, kv8, pairs, st);
@@ -344,9 +345,9 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   p.idx = idx;
   p.new_len = new_len;
   // CTAs a row: as many as let every row run at once, up to a portable cluster
-  // (16 rows of 131072 positions: two waves of clusters of 8 took 82 us, one of
-  // clusters of 6 takes 54).  More rows than SMs: smaller CTAs, two an SM (256
-  // rows of 2000: 69 us against 84).
+  // (16 rows of 131072 positions: two waves of clusters of 8 take 80 us, one of
+  // clusters of 6 53).  More rows than SMs: smaller CTAs, two an SM (256 rows of
+  // 2000: 69 us against 88).
   const int64_t rows = static_cast<int64_t>(cache->n_seqs) * cache->Hkv;
   int ctas = EV_MAX_CTAS;
   while (ctas > 1 && rows > active_clusters(ctas)) --ctas;
@@ -399,7 +400,7 @@ int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const
   p.flags = g_flags;
   // at least one item per KV head for every tile (pair) any split of total_q
   // tokens into n_seqs sequences can have; single tiles while all of them run
-  // at once
+  // at once (7 short prompts: 12.4 us, in pairs 14.4)
   const int64_t singles = s->total_q / p.rows_tok + s->n_seqs;
   p.tiles = singles * s->Hkv <= sm_count() ? 1 : 2;
   const int64_t items = p.tiles == 1 ? singles : s->total_q / (2 * p.rows_tok) + s->n_seqs;

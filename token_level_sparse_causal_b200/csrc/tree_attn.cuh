@@ -186,7 +186,8 @@ struct TreeWalk {
 // One warp splits all key tiles evenly over the CTAs and finds where this CTA's
 // stretch begins.  units: a sequence's keys count once per token tile.  over:
 // cost of a unit beside its tiles (queries to load, a pipeline to fill, an O to
-// write); without it the CTAs with many short sequences came in last.
+// write); without it the CTAs with many short sequences came in last (64 of up to
+// 500 tokens: 34 us, 42 without).
 template <typename Bars>
 __device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool units, int over, int where) {
   const int lane = threadIdx.x & 31;

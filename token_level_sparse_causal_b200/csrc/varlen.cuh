@@ -29,7 +29,9 @@
 //            the last product reads them.
 //
 // Bound by the tensor cores and the serial chain through the softmax, as
-// kernel (1) is; short prompts by the latency of a CTA's few steps.
+// kernel (1) is (32/8 heads: one prompt of 32768 tokens 8.3 ms, 1060 TFLOP/s; 32
+// prompts of up to 4096 450 us, 910); short prompts by the latency of a CTA's
+// few steps (7 of them 12.4 us).
 #pragma once
 
 #include "attn_tile.cuh"
