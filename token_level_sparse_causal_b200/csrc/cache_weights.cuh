@@ -12,35 +12,34 @@
 // in tree_attn.cuh, but by (sequence, KV head): a CTA takes an equal stretch of
 // all key tiles, and for more than CW_ROWS rows walks its part of a sequence
 // once per CW_ROWS rows (adding to what it wrote; the K tiles then come from
-// L2).  Of a
-// bf16 cache two pairs of epilogue warpgroups take the even and the odd tiles,
-// each warpgroup half of the columns (with one a tile 32 columns took 700
-// cycles of mostly waiting); the second hands its sums to the first through
-// shared memory.  An e4m3 cache leaves registers for one warpgroup a tile
-// beside the converting warps.  Bound by memory up to about 100 rows (bf16, 4 x
-// 32768 tokens of 64/8 heads: 8 rows 51 us, 5.4 TB/s; 128 rows 61 us, 4.5), then
-// by the exponentials (512 rows 191 us): 16 a clock and SM on the MUFU unit, so
-// where all 32 columns of a chunk count six of its sixteen pairs take the
-// degree-4 polynomial on the FMA pipes instead (2.6e-6; the cubic that kernel
-// (2) mixes in is exact only to 7.5e-5).
+// L2).  Two pairs of epilogue warpgroups take the even and the odd tiles, each
+// warpgroup half of the columns (with one a tile 32 columns took 700 cycles of
+// mostly waiting); the second hands its sums to the first through shared memory.
 //
-// e4m3: codes arrive by TMA in a raw ring and are turned into bf16 by eight
-// warps; the key's scale multiplies its row of scores.  Bound by the conversion
-// at few rows (60 us, 2.4 TB/s), by the sums of the one warpgroup a tile at many
-// (128 rows 89 us, 512 rows 277).
+// e4m3: the codes are an operand of the product as they arrive (kind::f8f6f4).
+// A query row times a power of two is the sum of two e4m3 rows (weights_split_q),
+// so eight products of 32 give the scores that eight of 16 give in bf16; the
+// key's scale and the row's power of two multiply them afterwards.  Turning the
+// codes into bf16 instead took 245 us for 4 x 131072 tokens and 128 rows, where
+// this takes 188.
+//
+// Bound by memory at few rows (4 x 32768 tokens of 64/8 heads, 8 rows: bf16 50
+// us, 5.5 TB/s; e4m3 44 us, 3.3 TB/s, there the steps of a tile are longer than
+// its load), then by the exponentials (512 rows: 187 and 223 us): 16 a clock and
+// SM on the MUFU unit, so where all 32 columns of a chunk count four
+// of its sixteen pairs take the degree-4 polynomial on the FMA pipes instead
+// (2.6e-6; the cubic that kernel (2) mixes in is exact only to 7.5e-5; none of
+// them 199 and 235 us, eight 202 and 257).
 #pragma once
 
+#include "quantize.cuh"
 #include "tree_attn.cuh"
 
 namespace hs2 {
 
-constexpr int CW_ROWS = 256;     // query rows of a pass; 128 of them: 222 us for 192 with 512 rows of a
-                                 // bf16 cache (above), 326 for 277 of an e4m3 one, 58 for 60 with 8 rows
-constexpr int CW_MAX_ITEMS = 4;  // K tiles in the ring, at most
-constexpr int CW_MAX_RAW = 5;    // e4m3: raw tiles, at most
-constexpr int CW_CONV = 256;     // e4m3: converting threads
-__host__ __device__ constexpr int cw_halves(bool kv8) { return kv8 ? 1 : 2; }  // epilogue warpgroups of a tile
-__host__ __device__ constexpr int cw_threads(bool kv8) { return 128 + 256 * cw_halves(kv8) + (kv8 ? CW_CONV : 0); }
+constexpr int CW_ROWS = 256;     // query rows of a pass (128: 222 us for 192 with 512 rows of a bf16 cache)
+constexpr int CW_MAX_ITEMS = 8;  // K tiles in the ring, at most
+constexpr int CW_THREADS = 640;  // loads, products, queries and a spare warp; two warpgroups for each tile parity
 
 struct WeightParams {
   TreeParams t;          // geometry, table, cu, ctx, mask, scales, limits
@@ -48,11 +47,12 @@ struct WeightParams {
   const uint8_t* counted;
   float* acc;            // [B][Hkv][acc_stride]
   int64_t acc_stride;
+  const __nv_bfloat16* q;  // e4m3 only (else by TMA)
+  int64_t q_tok, q_head;
 };
 
 struct WeightBars {
   uint64_t full[CW_MAX_ITEMS], empty[CW_MAX_ITEMS];
-  uint64_t raw_full[CW_MAX_RAW], raw_empty[CW_MAX_RAW];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t rows_ready[2];
@@ -69,19 +69,19 @@ static_assert(sizeof(WeightBars) <= 512, "barrier area");
 template <bool KV8>
 struct WeightSmem {
   static constexpr int QR = CW_ROWS;
-  static constexpr int ITEMS = KV8 ? 2 : 4;
-  static constexpr int RAWS = 5;
-  static_assert(ITEMS <= CW_MAX_ITEMS && RAWS <= CW_MAX_RAW, "rings");
-  static constexpr uint32_t QHALF = QR * 128u;
-  static constexpr uint32_t ITEM = 2 * QHALF;  // after Q
-  static constexpr uint32_t RAW = ITEM + ITEMS * TILE_BYTES;
-  static constexpr uint32_t BAR = RAW + (KV8 ? RAWS * RAW_BYTES : 0u);
+  static constexpr int ITEMS = KV8 ? 8 : 4;
+  static_assert(ITEMS <= CW_MAX_ITEMS, "ring");
+  static constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
+  static constexpr uint32_t QHALF = QR * 128u;  // half of d in bf16, or one of the two e4m3 parts
+  static constexpr uint32_t ITEM = 2 * QHALF;   // after Q
+  static constexpr uint32_t BAR = ITEM + ITEMS * SLOT;
   // per epilogue warpgroup and segment parity, for each column (query row):
   static constexpr uint32_t BITS = BAR + 512u;                // uint64 [2][2][QR]: the drafted keys it sees
   static constexpr uint32_t NLSE = BITS + 2 * 2 * QR * 8u;    // float [2][2][QR]: -lse * log2(e), -inf: none
   static constexpr uint32_t LIVE = NLSE + 2 * 2 * QR * 4u;    // uint32 [2][2][QR / 32]: the columns that collect
   static constexpr uint32_t PART = LIVE + 2 * 2 * QR / 8u;    // float [2][128]
-  static constexpr uint32_t BYTES = PART + 1024u;
+  static constexpr uint32_t QSC = PART + 1024u;               // e4m3: float [2][QR], what a column's scores are multiplied by
+  static constexpr uint32_t BYTES = QSC + (KV8 ? 2 * QR * 4u : 0u);
   static_assert(BYTES <= 232448u, "shared memory of one CTA");
 };
 
@@ -131,34 +131,91 @@ struct WeightWalk {
   __device__ __forceinline__ int n() const { return t1 - t0; }
 };
 
+// Rows [0, rows) of a pass's queries as e4m3 pairs, by the 16 warps of the
+// sums (w): a bf16 value has 8 significant bits, two e4m3 values of 4 hold it
+// where it is not below 2^-9 of the row's maximum (then the error is at most
+// 2^-18 of that maximum).  The row is scaled by the power of two that brings its
+// maximum to [128, 256).
+__device__ __forceinline__ void weights_split_q(const WeightParams& wp, uint8_t* smem, uint32_t qhalf, float* qsc,
+                                                int g, int64_t row0, int rows, int w) {
+  const int lane = threadIdx.x & 31, l16 = lane & 15;
+  constexpr int STEPS = CW_ROWS / 32;
+  uint4 raw[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int c = 32 * s + 2 * w + (lane >> 4);
+    raw[s] = make_uint4(0, 0, 0, 0);
+    if (c < rows)
+      raw[s] = *reinterpret_cast<const uint4*>(wp.q + (row0 + c / wp.t.G) * wp.q_tok +
+                                               (g * wp.t.G + c % wp.t.G) * wp.q_head + 8 * l16);
+  }
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    if (32 * s >= rows) break;
+    const int c = 32 * s + 2 * w + (lane >> 4);
+    const uint32_t v[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+    uint32_t top = 0;  // the exponents' maximum, in bits 7 .. 14
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7f80u, (v[e] >> 16) & 0x7f80u));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t eb = max(top >> 7, 8u);
+    const float up = __uint_as_float(min(261u - eb, 254u) << 23);
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = __uint_as_float(v[e] << 16) * up, y = __uint_as_float(v[e] & 0xffff0000u) * up;
+      const uint32_t a = e4m3x2_from_f32(x, y), h = e4m3x2_to_f16x2(a);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      const uint32_t b = e4m3x2_from_f32(x - f.x, y - f.y);
+      if (e & 1) {
+        hi[e >> 1] |= a << 16;
+        lo[e >> 1] |= b << 16;
+      } else {
+        hi[e >> 1] = a;
+        lo[e >> 1] = b;
+      }
+    }
+    if (c < rows) {
+      uint8_t* dst = smem + sw128_chunk_offset(c, l16 >> 1, 0) + 8 * (l16 & 1);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + qhalf) = make_uint2(lo[0], lo[1]);
+    }
+    if (l16 == 0) qsc[c] = __uint_as_float((eb - 7u) << 23);  // columns behind the rows too: their scores of 0 stay 0
+  }
+}
+
 // Adds 32 columns' weights of one key to sum.  ALL: every column collects, so
 // that some exponentials may leave the MUFU unit (the polynomial has no zero
 // for a column that does not; skipping such columns eight at a time cost more
 // in branches than it saved).
-template <bool ALL>
+template <bool KV8, bool ALL>
 __device__ __forceinline__ void weights_add(const uint32_t (&sr)[32], uint64_t f2, const float* nlse,
-                                            uint64_t (&sum)[4]) {
+                                            const float* qsc, uint64_t (&sum)[4]) {
   const float4* nl4 = reinterpret_cast<const float4*>(nlse);
+  const float4* qs4 = reinterpret_cast<const float4*>(qsc);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float4 nl = nl4[e];  // broadcast
+    const float4 qs = KV8 ? qs4[e] : make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int c = 4 * e + 2 * i, pair = 2 * e + i;
-      const uint64_t x = f2_fma(f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2,
-                                i ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y));
-      const bool poly = ALL && (pair % 8 == 1 || pair % 8 == 4 || pair % 8 == 6);
+      uint64_t score = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+      if (KV8) score = f2_mul(score, i ? f2_pack(qs.z, qs.w) : f2_pack(qs.x, qs.y));
+      const uint64_t x = f2_fma(score, f2, i ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y));
+      const bool poly = ALL && pair % 4 == 1;
       sum[pair & 3] = f2_add(sum[pair & 3], poly ? exp2_fma_x2<4>(x) : ex2_x2(x));
     }
   }
 }
 
 template <bool KV8>
-__global__ void __launch_bounds__(cw_threads(KV8), 1)
+__global__ void __launch_bounds__(CW_THREADS, 1)
     cache_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const WeightParams wp) {
   using SM = WeightSmem<KV8>;
-  constexpr int QR = SM::QR, ITEMS = SM::ITEMS, RAWS = SM::RAWS, HALVES = cw_halves(KV8);
+  constexpr int QR = SM::QR, ITEMS = SM::ITEMS;
   const TreeParams& p = wp.t;
   extern __shared__ __align__(1024) uint8_t weights_smem[];
   uint8_t* smem = weights_smem;
@@ -173,21 +230,15 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ITEMS; ++s) {
-      mbar_init(&bars->full[s], KV8 ? CW_CONV / 32 : 1);
+      mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
-    if (KV8) {
-      for (int s = 0; s < RAWS; ++s) {
-        mbar_init(&bars->raw_full[s], 1);
-        mbar_init(&bars->raw_empty[s], CW_CONV / 32);
-      }
-    }
-    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_full, KV8 ? 16 : 1);
     mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->s_empty[x], 4 * HALVES);
-      mbar_init(&bars->rows_ready[x], 4 * HALVES);
+      mbar_init(&bars->s_empty[x], 8);
+      mbar_init(&bars->rows_ready[x], 8);
       mbar_init(&bars->part_full[x], 4);
       mbar_init(&bars->part_empty[x], 4);
     }
@@ -211,11 +262,6 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
     // ======================================================== K tiles by TMA
     WeightWalk w;
     const bool work = !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars);
-    constexpr int RING = KV8 ? RAWS : ITEMS;
-    constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
-    uint64_t* full = KV8 ? bars->raw_full : bars->full;
-    uint64_t* empty = KV8 ? bars->raw_empty : bars->empty;
-    uint8_t* ring = smem + (KV8 ? SM::RAW : SM::ITEM);
     const int page = 1 << p.page_log2, per_tile = 128 >> p.page_log2;
     int item = 0;
     bool ok = work;
@@ -229,24 +275,24 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
       int pg = page_of(w.t0);
       for (int t = w.t0; t < w.t1; ++t, ++item) {
         const int next_pg = page_of(t + 1);
-        const int slot = item % RING;
-        if (item >= RING && !warp_wait(&empty[slot], ((item / RING) - 1) & 1, p.limit_ns, abort_flag, 911)) {
+        const int slot = item % ITEMS;
+        if (item >= ITEMS && !warp_wait(&bars->empty[slot], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 911)) {
           ok = false;
           break;
         }
         const int keys = min(128, len - t * 128);
         const int pages = (keys + page - 1) >> p.page_log2;
         if (lane == 0)
-          mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(pages << p.page_log2) * (KV8 ? 128u : 256u));
+          mbar_arrive_expect_tx(&bars->full[slot], static_cast<uint32_t>(pages << p.page_log2) * (KV8 ? 128u : 256u));
         __syncwarp();
         if (lane < pages) {
           if (pg < 0 || pg >= p.n_pages) {
             report(HS2_ERR_INDEX, 912);
             pg = p.n_pages;
           }
-          uint8_t* dst = ring + slot * SLOT + lane * page * 128;
-          tma_load_3d(dst, &tmK, &full[slot], 0, w.g, pg << p.page_log2);
-          if (!KV8) tma_load_3d(dst + HALF_BYTES, &tmK, &full[slot], 64, w.g, pg << p.page_log2);
+          uint8_t* dst = smem + SM::ITEM + slot * SM::SLOT + lane * page * 128;
+          tma_load_3d(dst, &tmK, &bars->full[slot], 0, w.g, pg << p.page_log2);
+          if (!KV8) tma_load_3d(dst + HALF_BYTES, &tmK, &bars->full[slot], 64, w.g, pg << p.page_log2);
         }
         pg = next_pg;
       }
@@ -254,50 +300,62 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
     }
     __syncwarp();
     if (lane == 0 && work)
-      for (int u = max(0, item - RING); u < item; ++u)
-        wait_done(&full[u % RING], (u / RING) & 1, p.limit_ns, 913);
+      for (int u = max(0, item - ITEMS); u < item; ++u)
+        wait_done(&bars->full[u % ITEMS], (u / ITEMS) & 1, p.limit_ns, 913);
   } else if (warp == 1) {
     // ========================================================== MMA issue
+    // by the elected lane of a warp that walks together (as one lane's branch the
+    // issue took longer than the load of a tile: e4m3, 8 rows 56 us for 44)
     WeightWalk w;
-    if (lane == 0 && w.begin(p, bars)) {
-      int item = 0, seg = 0, used[2] = {0, 0};
+    if (w.begin(p, bars)) {
+      int item = 0, seg = 0;
+      uint32_t used = 0, uses = 0;  // by tile parity: whether a tile was issued, and how many (mod 2)
       bool ok = true;
       while (ok) {
-        if (!(ok = mbar_wait(&bars->q_full, seg & 1, p.limit_ns, abort_flag, 921))) break;
+        if (!(ok = warp_wait(&bars->q_full, seg & 1, p.limit_ns, abort_flag, 921))) break;
         const int rows = min(p.R, w.T - w.m * p.R) * p.G;
         const uint32_t cols = static_cast<uint32_t>((rows + 15) & ~15);
-        const uint32_t idesc = idesc_bf16_f32(128, static_cast<int>(cols), 0, 0);
+        const uint32_t idesc = KV8 ? idesc_e4m3_f32(128, static_cast<int>(cols))
+                                   : idesc_bf16_f32(128, static_cast<int>(cols), 0, 0);
         const int n = w.n();
         for (int j = 0; j < n; ++j, ++item) {
           const int x = j & 1, slot = item % ITEMS;
-          ok = mbar_wait(&bars->full[slot], (item / ITEMS) & 1, p.limit_ns, abort_flag, 922) &&
-               (used[x] == 0 || mbar_wait(&bars->s_empty[x], (used[x] - 1) & 1, p.limit_ns, abort_flag, 923));
+          ok = warp_wait(&bars->full[slot], (item / ITEMS) & 1, p.limit_ns, abort_flag, 922) &&
+               (!(used >> x & 1u) ||
+                warp_wait(&bars->s_empty[x], ~(uses >> x) & 1u, p.limit_ns, abort_flag, 923));
           if (!ok) break;
-          ++used[x];
+          used |= 1u << x;
+          uses ^= 1u << x;
           tc_fence_after();
-          const uint32_t kb = item_base + slot * TILE_BYTES;
+          const uint64_t da = sdesc_sw128(item_base + slot * SM::SLOT, 16, 1024), db = sdesc_sw128(q_base, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-            const uint32_t qoff = (kk >> 2) * SM::QHALF + (kk & 3) * 32;
-            umma_ss(tmem + x * QR, sdesc_sw128(kb + koff, 16, 1024), sdesc_sw128(q_base + qoff, 16, 1024), idesc,
-                    kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk) {  // e4m3: the same keys times both parts of the queries
+              const uint32_t koff = (KV8 ? 0 : (kk >> 2) * HALF_BYTES) + (kk & 3) * 32;
+              const uint32_t qoff = (kk >> 2) * SM::QHALF + (kk & 3) * 32;
+              if (KV8)
+                umma_ss_f8(tmem + x * QR, da + (koff >> 4), db + (qoff >> 4), idesc, kk > 0 ? 1u : 0u);
+              else
+                umma_ss(tmem + x * QR, da + (koff >> 4), db + (qoff >> 4), idesc, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bars->s_full[x]);
+            umma_commit(&bars->empty[slot]);
+            if (j == n - 1) umma_commit(&bars->q_empty);
           }
-          umma_commit(&bars->s_full[x]);
-          umma_commit(&bars->empty[slot]);
+          __syncwarp();
         }
         if (!ok) break;
-        umma_commit(&bars->q_empty);
         ++seg;
         if (!w.next(p)) break;
       }
-      umma_commit(&bars->fin);
+      if (elect_one()) umma_commit(&bars->fin);
+      __syncwarp();
       wait_done(&bars->fin, 0, p.limit_ns, 924);
     }
   } else if (warp == 3) {
-    // ======================================================= queries by TMA
+    // ========================================= bf16: queries by TMA
     WeightWalk w;
-    if (lane == 0 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
+    if (!KV8 && lane == 0 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
       const uint32_t half = static_cast<uint32_t>(p.R * p.G) * 128u;
       int seg = 0;
       do {
@@ -309,10 +367,10 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
       } while (w.next(p));
       wait_done(&bars->q_full, (seg - 1) & 1, p.limit_ns, 932);
     }
-  } else if (warp >= 4 && warp < 4 + 8 * HALVES) {
+  } else if (warp >= 4) {
     // ===== sums: thread r of a warpgroup owns key r of tiles x, x + 2, ..., and
-    // all or half of the columns
-    const int x = (warp - 4) / (4 * HALVES), half = HALVES == 1 ? 0 : ((warp - 4) >> 2) & 1;
+    // half of the columns
+    const int x = (warp - 4) >> 3, half = ((warp - 4) >> 2) & 1;
     const int r = (threadIdx.x - 128) & 127;
     const uint32_t s_tm = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * QR;
     float* part = reinterpret_cast<float*>(smem + SM::PART) + x * 128 + r;
@@ -328,8 +386,8 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
       uint64_t* row_bits = reinterpret_cast<uint64_t*>(smem + SM::BITS) + area * QR;
       float* row_nlse = reinterpret_cast<float*>(smem + SM::NLSE) + area * QR;
       uint32_t* live = reinterpret_cast<uint32_t*>(smem + SM::LIVE) + area * (QR / 32);
-#pragma unroll
-      for (int c = 128 * half + r; c < QR; c += 128 * HALVES) {
+      {
+        const int c = 128 * half + r;
         uint64_t bits = 0;
         float nl = -INFINITY;
         const int t = w.m * p.R + c / p.G;
@@ -345,9 +403,15 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
         const uint32_t m = __ballot_sync(0xffffffffu, nl != -INFINITY);
         if (lane == 0) live[c >> 5] = m;
       }
+      const float* qsc = reinterpret_cast<float*>(smem + SM::QSC) + (seg & 1) * QR;
+      if (KV8) {  // both tile parities' warps write the queries, when the last segment's products are done
+        if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 945)) break;
+        weights_split_q(wp, smem, SM::QHALF, const_cast<float*>(qsc), w.g, w.row0 + w.m * p.R, rows, warp - 4);
+        fence_proxy_async_smem();
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->rows_ready[x]);
-      if (!warp_wait(&bars->rows_ready[x], seg & 1, p.limit_ns, abort_flag, 942)) break;
+      if (lane == 0) mbar_arrive(KV8 ? &bars->q_full : &bars->rows_ready[x]);
+      if (!warp_wait(KV8 ? &bars->q_full : &bars->rows_ready[x], seg & 1, p.limit_ns, abort_flag, 942)) break;
       ++seg;
       const int len = w.ctx + w.T, n = w.n();
       const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
@@ -383,7 +447,7 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
         const bool drafted = __any_sync(0xffffffffu, d >= 0);
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
         const uint64_t ff = f2_pack(f, f);
-        const int chunks = (rows + 31) / 32, mid = HALVES == 1 ? chunks : (chunks + 1) / 2;
+        const int chunks = (rows + 31) / 32, mid = (chunks + 1) / 2;
         const int c_end = half ? chunks : mid;
 #pragma unroll 1
         for (int c = half ? mid : 0; c < c_end; ++c) {
@@ -402,13 +466,14 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const bool seen = d < 0 || (in_reach && (row_bits[c0 + e] >> (d & 63) & 1u));
-              const float y = ex2_approx(fmaf(__uint_as_float(sr[e]), f, row_nlse[c0 + e]));
+              const float score = __uint_as_float(sr[e]) * (KV8 ? qsc[c0 + e] : 1.f);
+              const float y = ex2_approx(fmaf(score, f, row_nlse[c0 + e]));
               sum[e & 3] = f2_add(sum[e & 3], f2_pack(seen ? y : 0.f, 0.f));
             }
           } else if (live[c] == 0xffffffffu) {
-            weights_add<true>(sr, ff, row_nlse + c0, sum);
+            weights_add<KV8, true>(sr, ff, row_nlse + c0, qsc + c0, sum);
           } else {
-            weights_add<false>(sr, ff, row_nlse + c0, sum);
+            weights_add<KV8, false>(sr, ff, row_nlse + c0, qsc + c0, sum);
           }
         }
         tc_fence_before();
@@ -418,7 +483,7 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
         f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
         f2_unpack(f2_add(sum[2], sum[3]), s2, s3);
         float total = (s0 + s1) + (s2 + s3);
-        if (HALVES > 1 && chunks > 1) {
+        if (chunks > 1) {
           if (half) {
             if (np > 0 && !(ok = warp_wait(&bars->part_empty[x], (np - 1) & 1, p.limit_ns, abort_flag, 943))) break;
             *part = total;
@@ -435,30 +500,6 @@ __global__ void __launch_bounds__(cw_threads(KV8), 1)
         if (!half && at < len) acc[at] = old + total;
       }
       if (!ok || !w.next(p)) break;
-    }
-  } else if (warp >= 4 + 8 * HALVES) {
-    // ================================================== e4m3: codes to bf16
-    WeightWalk w;
-    if (KV8 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
-      const int pt = threadIdx.x - 128 * (1 + 2 * HALVES);
-      const uint32_t raw_base = smem_u32(smem + SM::RAW);
-      int item = 0;
-      bool ok = true;
-      do {
-        for (int t = w.t0; t < w.t1 && ok; ++t, ++item) {
-          const int rs = item % RAWS, cs = item % ITEMS;
-          ok = warp_wait(&bars->raw_full[rs], (item / RAWS) & 1, p.limit_ns, abort_flag, 951) &&
-               (item < ITEMS || warp_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 952));
-          if (!ok) break;
-          convert_tile<CW_CONV>(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, w.ctx + w.T - t * 128, pt);
-          fence_proxy_async_smem();
-          __syncwarp();  // one arrival per warp: 256 of them would take longer than the conversion
-          if (lane == 0) {
-            mbar_arrive(&bars->full[cs]);
-            mbar_arrive(&bars->raw_empty[rs]);
-          }
-        }
-      } while (ok && w.next(p));
     }
   }
 

@@ -60,9 +60,9 @@ int check_cache(const hs2_cache* c, bool table) {
 }
 
 // 3-D map over e4m3 codes [tokens][heads][128], a box of one head's codes of
-// box_t tokens, not swizzled.
+// box_t tokens, swizzled (128 bytes) where the tensor cores read them.
 int make_map_codes(CUtensorMap* m, const void* base, int64_t L, int H, int64_t tok_stride, int64_t head_stride,
-                   int box_t) {
+                   int box_t, bool swizzled) {
   EncodeTiledFn enc = encode_fn();
   if (!enc || (g_flags & FLAG_FAIL_TMAP)) return HS2_ERR_CUDA;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(HD), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(L)};
@@ -70,16 +70,18 @@ int make_map_codes(CUtensorMap* m, const void* base, int64_t L, int H, int64_t t
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(HD), 1u, static_cast<cuuint32_t>(box_t)};
   const cuuint32_t es[3] = {1u, 1u, 1u};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? HS2_OK : HS2_ERR_CUDA;
 }
 
 // A map over a pool of the cache, one box per page.
-int make_pool_map(CUtensorMap* m, const hs2_cache* c, const void* pool) {
+int make_pool_map(CUtensorMap* m, const hs2_cache* c, const void* pool, bool codes_swizzled = false) {
   const int tokens = c->n_pages * c->page;
   return c->kv_dtype == HS2_KV_E4M3
-             ? make_map_codes(m, pool, tokens, c->Hkv, c->tok_stride, c->head_stride, c->page)
+             ? make_map_codes(m, pool, tokens, c->Hkv, c->tok_stride, c->head_stride, c->page,
+                              codes_swizzled)
              : make_map(m, pool, tokens, c->Hkv, c->tok_stride, c->head_stride, 1, c->page);
 }
 
@@ -235,7 +237,7 @@ template <bool KV8>
 int launch_weights(const CUtensorMap& mq, const CUtensorMap& mk, const WeightParams& p, cudaStream_t st) {
   constexpr uint32_t smem = WeightSmem<KV8>::BYTES;
   if (int rc = set_smem(cache_weights_kernel<KV8>, smem)) return rc;
-  cache_weights_kernel<KV8><<<static_cast<unsigned>(sm_count()), cw_threads(KV8), smem, st>>>(mq, mk, p);
+  cache_weights_kernel<KV8><<<static_cast<unsigned>(sm_count()), CW_THREADS, smem, st>>>(mq, mk, p);
   return launched();
 }
 
@@ -485,10 +487,13 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   p.acc = acc;
   p.acc_stride = acc_stride;
   p.t.max_len = std::min(p.t.max_len, acc_stride);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_tok = draft->q_tok_stride;
+  p.q_head = draft->q_head_stride;
   CUtensorMap mq, mk;
   if (int rc = make_map(&mq, q, draft->n_tok, draft->Hq, draft->q_tok_stride, draft->q_head_stride, p.t.G, p.t.R))
     return rc;
-  if (int rc = make_pool_map(&mk, cache, cache->k)) return rc;
+  if (int rc = make_pool_map(&mk, cache, cache->k, true)) return rc;
   const Range range("hs2 cache_weights");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cache->kv_dtype == HS2_KV_E4M3 ? launch_weights<true>(mq, mk, p, st) : launch_weights<false>(mq, mk, p, st);
