@@ -1,7 +1,7 @@
 // Causal grouped-query attention over packed prompts of different lengths.
 // Per sequence o_i = softmax_{j <= i + nk - nq} (q_i . k_j / sqrt(d)) v_j.
 //
-// The pipeline is kernel (1)'s (flash.cuh: TMA loads, one MMA-issuing thread,
+// The pipeline is kernel (1)'s (flash.cuh: TMA loads, one MMA-issuing lane,
 // two softmax warpgroups taking turns, S / P / O in tensor memory); what
 // differs is the shape of the work:
 //
@@ -29,8 +29,8 @@
 //            the last product reads them.
 //
 // Bound by the tensor cores and the serial chain through the softmax, as
-// kernel (1) is (32/8 heads: one prompt of 32768 tokens 8.3 ms, 1060 TFLOP/s; 32
-// prompts of up to 4096 450 us, 910); short prompts by the latency of a CTA's
+// kernel (1) is (32/8 heads: one prompt of 32768 tokens 7.9 ms, 1110 TFLOP/s; 32
+// prompts of up to 4096 425 us, 970); short prompts by the latency of a CTA's
 // few steps (7 of them 12.4 us).
 #pragma once
 
@@ -420,70 +420,83 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
       }
     } else if (warp == 1) {
       // ========================================================== MMA issue
-      if (lane == 0) {
-        VarlenItem item;
-        int u = 0, nq_loads = 0, np[2] = {0, 0};
-        auto issue_s = [&](int x, int tile) {
-          const uint32_t kb = kv_base + (tile % FL_STAGES) * 2 * TILE_BYTES;
-          const uint32_t qb = q_base + x * TILE_BYTES;
-  #pragma unroll
+      // the warp walks together, its elected lane issues (as one lane's branch
+      // every case took 5 to 7% longer)
+      VarlenItem item;
+      int u = 0, nq_loads = 0;
+      uint32_t np = 0;  // by tile of the item: P tiles so far (mod 2)
+      auto issue_s = [&](int x, int tile) {
+        const uint64_t da = sdesc_sw128(q_base + x * TILE_BYTES, 16, 1024);
+        const uint64_t db = sdesc_sw128(kv_base + (tile % FL_STAGES) * 2 * TILE_BYTES, 16, 1024);
+        if (elect_one()) {
+#pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-            umma_ss(tmem + x * 128, sdesc_sw128(qb + koff, 16, 1024), sdesc_sw128(kb + koff, 16, 1024), IDESC_S,
-                    kk > 0 ? 1u : 0u);
+            const uint32_t koff = ((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4;
+            umma_ss(tmem + x * 128, da + koff, db + koff, IDESC_S, kk > 0 ? 1u : 0u);
           }
           umma_commit(&bars->s_full[x]);
-        };
-        auto issue_pv = [&](int x, int tile, bool first, bool last) {
-          const uint32_t vb = kv_base + (tile % FL_STAGES) * 2 * TILE_BYTES + TILE_BYTES;
-  #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 2048, HALF_BYTES, 1024),
-                    IDESC_PV, (!first || kk > 0) ? 1u : 0u);
-          if (last) umma_commit(&bars->o_done[x]);
-        };
-        auto k_landed = [&](int tile) {
-          return mbar_wait(&bars->full_k[tile % FL_STAGES], (tile / FL_STAGES) & 1, p.limit_ns, abort_flag, 721);
-        };
-        bool ok = true;
-        for (int it = 0; ok && item_of(it, item); ++it) {
-          const VarlenTiles t(item, R, p.tiles);
-          const int n = t.n, nx[2] = {t.nA, t.nB};
-          if (n > 0) {
-            ok = mbar_wait(&bars->q_full, nq_loads++ & 1, p.limit_ns, abort_flag, 722) && k_landed(u);
-            if (!ok) break;
-            tc_fence_after();
-            for (int x = 0; x < 2; ++x)
-              if (nx[x] > 0) issue_s(x, u);
-            umma_commit(&bars->empty_k[u % FL_STAGES]);
-            if (n == 1) umma_commit(&bars->q_empty);
-          }
-          // the last item's O has been read (waited for at every item, as each
-          // has its phase)
-          if (it > 0 && !(ok = mbar_wait(&bars->o_free, (it - 1) & 1, p.limit_ns, abort_flag, 723))) break;
-          for (int j = 0; j < n && ok; ++j) {
-            const int tile = u + j, s = tile % FL_STAGES;
-            ok = mbar_wait(&bars->full_v[s], (tile / FL_STAGES) & 1, p.limit_ns, abort_flag, 724) &&
-                 (j + 1 >= n || k_landed(tile + 1));
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (j >= nx[x]) continue;
-              if (!(ok = mbar_wait(&bars->p_ready[x], np[x]++ & 1, p.limit_ns, abort_flag, 725))) break;
-              tc_fence_after();
-              issue_pv(x, tile, j == 0, j == nx[x] - 1);
-              if (j + 1 < nx[x]) issue_s(x, tile + 1);
-            }
-            if (ok) {
-              umma_commit(&bars->empty_v[s]);
-              if (j + 1 < n) umma_commit(&bars->empty_k[(tile + 1) % FL_STAGES]);
-              if (j + 2 == n) umma_commit(&bars->q_empty);  // every score product is queued
-            }
-          }
-          u += n;
-          if (ok) mbar_arrive(&bars->item_empty[it % VL_ITEMS]);
         }
-        umma_commit(&bars->fin);
-        wait_done(&bars->fin, 0, p.limit_ns, 726);
+        __syncwarp();
+      };
+      auto issue_pv = [&](int x, int tile, bool first, bool last) {
+        const uint64_t db =
+            sdesc_sw128(kv_base + (tile % FL_STAGES) * 2 * TILE_BYTES + TILE_BYTES, HALF_BYTES, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, db + kk * (2048 >> 4), IDESC_PV,
+                    (!first || kk > 0) ? 1u : 0u);
+          if (last) umma_commit(&bars->o_done[x]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      auto k_landed = [&](int tile) {
+        return warp_wait(&bars->full_k[tile % FL_STAGES], (tile / FL_STAGES) & 1, p.limit_ns, abort_flag, 721);
+      };
+      bool ok = true;
+      for (int it = 0; ok && __all_sync(0xffffffffu, item_of(it, item)); ++it) {
+        const VarlenTiles t(item, R, p.tiles);
+        const int n = t.n;
+        if (n > 0) {
+          ok = warp_wait(&bars->q_full, nq_loads++ & 1, p.limit_ns, abort_flag, 722) && k_landed(u);
+          if (!ok) break;
+          tc_fence_after();
+          if (t.nA > 0) issue_s(0, u);
+          if (t.nB > 0) issue_s(1, u);
+          commit(&bars->empty_k[u % FL_STAGES]);
+          if (n == 1) commit(&bars->q_empty);
+        }
+        // the last item's O has been read (waited for at every item, as each
+        // has its phase)
+        if (it > 0 && !(ok = warp_wait(&bars->o_free, (it - 1) & 1, p.limit_ns, abort_flag, 723))) break;
+        for (int j = 0; j < n && ok; ++j) {
+          const int tile = u + j, s = tile % FL_STAGES;
+          ok = warp_wait(&bars->full_v[s], (tile / FL_STAGES) & 1, p.limit_ns, abort_flag, 724) &&
+               (j + 1 >= n || k_landed(tile + 1));
+          for (int x = 0; x < 2 && ok; ++x) {
+            const int nx = x ? t.nB : t.nA;
+            if (j >= nx) continue;
+            if (!(ok = warp_wait(&bars->p_ready[x], (np >> x) & 1, p.limit_ns, abort_flag, 725))) break;
+            np ^= 1u << x;
+            tc_fence_after();
+            issue_pv(x, tile, j == 0, j == nx - 1);
+            if (j + 1 < nx) issue_s(x, tile + 1);
+          }
+          if (ok) {
+            commit(&bars->empty_v[s]);
+            if (j + 1 < n) commit(&bars->empty_k[(tile + 1) % FL_STAGES]);
+            if (j + 2 == n) commit(&bars->q_empty);  // every score product is queued
+          }
+        }
+        u += n;
+        if (ok && lane == 0) mbar_arrive(&bars->item_empty[it % VL_ITEMS]);
       }
+      commit(&bars->fin);
+      wait_done(&bars->fin, 0, p.limit_ns, 726);
     } else if (warp == 2) {
       // ==================================== V rows behind the sequence's end
       if (!(p.flags & FLAG_SKIP_LOADS)) {
