@@ -103,7 +103,7 @@ template <int NQ, bool SCALED, bool MASKED>
 __device__ __forceinline__ bool softmax_quarters(uint32_t s_tm, int q0, float sc, const float* kscale,
                                                  const float* vscale, const uint32_t (&vis)[4], RowState& st,
                                                  float& alpha) {
-  static_assert(NQ == 1 || NQ == 2 || NQ == 4, "quarters");
+  static_assert(NQ == 1 || NQ == 4, "quarters");
   uint32_t buf[2][32];
   auto issue = [&](int q, uint32_t(&sr)[32]) { tmem_ld32(s_tm + 32 * q, sr); };
   auto arrived = [&](uint32_t(&sr)[32]) {

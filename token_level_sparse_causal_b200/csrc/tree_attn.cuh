@@ -5,7 +5,7 @@
 // Bound by memory: K and V are read once (512 B per key and KV head in bf16,
 // 264 B as e4m3 with scales), and at T * G <= 128 rows one pass over them
 // serves all rows.  So the design is about keeping loads in flight (bf16,
-// 4 x 32768 tokens of 64/8 heads: T = 1 93 us, 5.8 TB/s; T = 16 107 us, 5.0):
+// 4 x 32768 tokens of 64/8 heads: T = 1 92 us, 5.8 TB/s; T = 16 106 us, 5.1):
 //
 //   work     the unit is (sequence, KV head, tile of RB / G tokens); all units'
 //            key tiles (128 keys) are laid end to end and every CTA (one per
@@ -22,20 +22,19 @@
 //            (own S, P, O in tensor memory, own warpgroup) that take turns on
 //            the tensor core as in flash.cuh; their O join in the epilogue,
 //            where each warpgroup writes half of the columns;
-//   few rows a tile's 128 rows are 4 blocks of 32 (2 of 64) copies of the unit's
+//   few rows a tile's 128 rows are 4 blocks of 32, copies of the unit's
 //            rows where those fit, and block k keeps only its share of the
 //            tile's keys (the rest of its P is zero): all warps share one row's
 //            exponentials, instead of one warp taking all of them (T = 1, e4m3
-//            cache of 4 x 32768 tokens 137 -> 111 us; bf16 64 short sequences
-//            37.4 -> 35.5 us, but 4 x 32768 91.9 -> 92.9 and one sequence of 2048
-//            13.7 -> 14.3, for the blocks' O to be added). Each block is a
+//            cache of 4 x 32768 tokens 121 -> 107 us; bf16 64 short sequences
+//            36 -> 32.5 us, one of 2048 tokens 14 -> 13). Each block is a
 //            softmax of its own; the epilogue adds the blocks' O, each block a
 //            share of the columns;
 //   e4m3     codes arrive by TMA in a raw ring; eight warps turn them into bf16
 //            (exact; unlike f16 it leaves Q and P their whole range), another
 //            fetches the scales; the K scale multiplies the scores, the V
 //            scale multiplies P before its rounding. Bound by that softmax and
-//            the conversion, not by memory: 2.1 TB/s at 128 rows, 2.5 at 8;
+//            the conversion, not by memory: 2.4 TB/s at 128 rows, 2.6 at 8;
 //   edges    columns without a visible key become -inf whatever they hold, V
 //            rows behind the last key are zeroed before the product.
 #pragma once
@@ -51,7 +50,7 @@ constexpr int TR_MAX_RAW = 5;    // e4m3: raw tiles of 16 KB, at most
 constexpr int TR_OVERHEAD = 3;   // what a unit costs beside its key tiles, in tiles (see tree_split)
 constexpr int TR_SCALES = 8;     // e4m3: key tiles whose scales are held or on their way
 constexpr uint32_t RAW_BYTES = 128u * 128u;
-constexpr int TR_CONV = 256;     // e4m3: converting threads (4 x 131072 tokens, T = 16: 386 us, 128 of them 470)
+constexpr int TR_CONV = 256;     // e4m3: converting threads (4 x 131072 tokens, T = 16: 330 us, 128 of them 430)
 __host__ __device__ constexpr int tr_threads(bool kv8) { return 384 + (kv8 ? TR_CONV : 0); }
 
 // What a call's kernels share: the unit geometry.
@@ -92,7 +91,7 @@ struct TreeBars {
 constexpr uint32_t TR_BAR_BYTES = 640;
 static_assert(sizeof(TreeBars) <= TR_BAR_BYTES, "barrier area");
 
-// RB: rows of a block (32, 64 or 128); a unit has RB / G tokens.
+// RB: rows of a block (32 or 128); a unit has RB / G tokens.
 template <bool KV8, int RB>
 struct TreeSmem {
   static constexpr int BLOCKS = 128 / RB;
@@ -703,36 +702,51 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
     } else if (warp == 1) {
       // ========================================================== MMA issue
       TreeWalk w;
-      if (lane == 0 && w.begin(p, bars)) {
-        int item = 0, seg = 0, np[2] = {0, 0};
+      if (w.begin(p, bars)) {  // the warp walks together, its elected lane issues
+        int item = 0, seg = 0;
+        uint32_t np = 0;  // by tile parity: tiles so far (mod 2)
         bool ok = true;
+        // One lane polls for few rows of an e4m3 cache (4 x 32768 tokens, T = 1: 107
+        // us, all lanes 119), all do otherwise (4 x 131072, T = 16: 331 us, one
+        // lane 344).
+        auto wait_for = [&](uint64_t* bar, uint32_t parity, int where) {
+          if constexpr (!KV8 || BLOCKS == 1) return warp_wait(bar, parity, p.limit_ns, abort_flag, where);
+          const bool mine = lane != 0 || mbar_wait(bar, parity, p.limit_ns, abort_flag, where);
+          return __all_sync(0xffffffffu, mine) != 0;
+        };
         auto wait_item = [&](int u) {
-          return mbar_wait(&bars->full[u % ITEMS], (u / ITEMS) & 1, p.limit_ns, abort_flag, 821);
+          return wait_for(&bars->full[u % ITEMS], (u / ITEMS) & 1, 821);
         };
         auto issue_s = [&](int x, int u, bool last) {
-          const uint32_t kb = item_base + (u % ITEMS) * TILE_BYTES;
+          const uint64_t da = sdesc_sw128(q_base, 16, 1024);
+          const uint64_t db = sdesc_sw128(item_base + (u % ITEMS) * TILE_BYTES, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t koff = (kk >> 2) * HALF_BYTES + (kk & 3) * 32;
-            umma_ss(tmem + x * 128, sdesc_sw128(q_base + koff, 16, 1024), sdesc_sw128(kb + koff, 16, 1024), IDESC_S,
-                    kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t koff = ((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4;
+              umma_ss(tmem + x * 128, da + koff, db + koff, IDESC_S, kk > 0 ? 1u : 0u);
+            }
+            umma_commit(&bars->s_full[x]);
+            umma_commit(&bars->empty[u % ITEMS]);
+            if (last) umma_commit(&bars->q_empty);
           }
-          umma_commit(&bars->s_full[x]);
-          umma_commit(&bars->empty[u % ITEMS]);
-          if (last) umma_commit(&bars->q_empty);
+          __syncwarp();
         };
         auto issue_pv = [&](int x, int u, bool first, bool last) {
-          const uint32_t vb = item_base + (u % ITEMS) * TILE_BYTES;
+          const uint64_t db = sdesc_sw128(item_base + (u % ITEMS) * TILE_BYTES, HALF_BYTES, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, sdesc_sw128(vb + kk * 2048, HALF_BYTES, 1024),
-                    IDESC_PV, (!first || kk > 0) ? 1u : 0u);
-          umma_commit(&bars->empty[u % ITEMS]);
-          if (last) umma_commit(&bars->o_done[x]);
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, db + kk * (2048 >> 4), IDESC_PV,
+                      (!first || kk > 0) ? 1u : 0u);
+            umma_commit(&bars->empty[u % ITEMS]);
+            if (last) umma_commit(&bars->o_done[x]);
+          }
+          __syncwarp();
         };
         while (ok) {
           const int n = w.n();
-          ok = mbar_wait(&bars->q_full, seg & 1, p.limit_ns, abort_flag, 822) && wait_item(item);
+          ok = wait_for(&bars->q_full, seg & 1, 822) && wait_item(item);
           if (!ok) break;
           tc_fence_after();
           issue_s(0, item++, n == 1);
@@ -748,8 +762,9 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
             // K(j + 2) may still be converted, so P V does not wait for it.
             ok = wait_item(item) && (KV8 || j + 2 >= n || wait_item(item + 1));
             // the last segment's O has been read
-            if (ok && j == 0 && seg > 0) ok = mbar_wait(&bars->o_free, (seg - 1) & 1, p.limit_ns, abort_flag, 824);
-            if (ok) ok = mbar_wait(&bars->p_ready[x], np[x]++ & 1, p.limit_ns, abort_flag, 825);
+            if (ok && j == 0 && seg > 0) ok = wait_for(&bars->o_free, (seg - 1) & 1, 824);
+            if (ok) ok = wait_for(&bars->p_ready[x], (np >> x) & 1, 825);
+            np ^= 1u << x;
             if (!ok) break;
             tc_fence_after();
             issue_pv(x, item++, j < 2, j + 2 >= n);
@@ -764,7 +779,8 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           ++seg;
           if (!ok || !w.next(p)) break;
         }
-        umma_commit(&bars->fin);
+        if (elect_one()) umma_commit(&bars->fin);
+        __syncwarp();
         wait_done(&bars->fin, 0, p.limit_ns, 826);
       }
     } else if (warp == 3) {
