@@ -120,6 +120,18 @@ def test_4096_sequences():
     _weights(c, rl)
 
 
+@pytest.mark.parametrize("drafts", [1, 4, 7])
+def test_many_short_e4m3_sequences(drafts):
+    """Units of one to three key tiles, several to a CTA: each role is a unit or more ahead of the next."""
+    rng = np.random.default_rng(drafts)
+    ctx = [int(x) for x in rng.choice([0, 1, 100, 124, 127, 128, 200, 255, 300], 150)]
+    c = Paged(ctx, [drafts] * 150, 16, 2, True, 16, drafts > 1, seed=30 + drafts).device(DEV)
+    for _ in range(3):
+        o, lse, gb = _attend(c)
+        rl = _check(c, o, lse, gb)
+    _weights(c, rl)
+
+
 def test_scales_of_any_size():
     """e4m3 caches whose scales are far from one: V around 1e-6 and 1e4, K that makes the same scores."""
     for f in (1e-6, 1e4):

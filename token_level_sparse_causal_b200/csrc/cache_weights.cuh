@@ -17,7 +17,7 @@
 // mostly waiting); the second hands its sums to the first through shared memory.
 //
 // e4m3: the codes are an operand of the product as they arrive (kind::f8f6f4).
-// A query row times a power of two is the sum of two e4m3 rows (weights_split_q),
+// A query row times a power of two is the sum of two e4m3 rows (split_queries),
 // so eight products of 32 give the scores that eight of 16 give in bf16; the
 // key's scale and the row's power of two multiply them afterwards.  Turning the
 // codes into bf16 instead took 245 us for 4 x 131072 tokens and 128 rows, where
@@ -32,7 +32,6 @@
 // them 199 and 235 us, eight 202 and 257).
 #pragma once
 
-#include "quantize.cuh"
 #include "tree_attn.cuh"
 
 namespace hs2 {
@@ -47,8 +46,6 @@ struct WeightParams {
   const uint8_t* counted;
   float* acc;            // [B][Hkv][acc_stride]
   int64_t acc_stride;
-  const __nv_bfloat16* q;  // e4m3 only (else by TMA)
-  int64_t q_tok, q_head;
 };
 
 struct WeightBars {
@@ -130,60 +127,6 @@ struct WeightWalk {
   }
   __device__ __forceinline__ int n() const { return t1 - t0; }
 };
-
-// Rows [0, rows) of a pass's queries as e4m3 pairs, by the 16 warps of the
-// sums (w): a bf16 value has 8 significant bits, two e4m3 values of 4 hold it
-// where it is not below 2^-9 of the row's maximum (then the error is at most
-// 2^-18 of that maximum).  The row is scaled by the power of two that brings its
-// maximum to [128, 256).
-__device__ __forceinline__ void weights_split_q(const WeightParams& wp, uint8_t* smem, uint32_t qhalf, float* qsc,
-                                                int g, int64_t row0, int rows, int w) {
-  const int lane = threadIdx.x & 31, l16 = lane & 15;
-  constexpr int STEPS = CW_ROWS / 32;
-  uint4 raw[STEPS];
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int c = 32 * s + 2 * w + (lane >> 4);
-    raw[s] = make_uint4(0, 0, 0, 0);
-    if (c < rows)
-      raw[s] = *reinterpret_cast<const uint4*>(wp.q + (row0 + c / wp.t.G) * wp.q_tok +
-                                               (g * wp.t.G + c % wp.t.G) * wp.q_head + 8 * l16);
-  }
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    if (32 * s >= rows) break;
-    const int c = 32 * s + 2 * w + (lane >> 4);
-    const uint32_t v[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
-    uint32_t top = 0;  // the exponents' maximum, in bits 7 .. 14
-#pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7f80u, (v[e] >> 16) & 0x7f80u));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const uint32_t eb = max(top >> 7, 8u);
-    const float up = __uint_as_float(min(261u - eb, 254u) << 23);
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = __uint_as_float(v[e] << 16) * up, y = __uint_as_float(v[e] & 0xffff0000u) * up;
-      const uint32_t a = e4m3x2_from_f32(x, y), h = e4m3x2_to_f16x2(a);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      const uint32_t b = e4m3x2_from_f32(x - f.x, y - f.y);
-      if (e & 1) {
-        hi[e >> 1] |= a << 16;
-        lo[e >> 1] |= b << 16;
-      } else {
-        hi[e >> 1] = a;
-        lo[e >> 1] = b;
-      }
-    }
-    if (c < rows) {
-      uint8_t* dst = smem + sw128_chunk_offset(c, l16 >> 1, 0) + 8 * (l16 & 1);
-      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(dst + qhalf) = make_uint2(lo[0], lo[1]);
-    }
-    if (l16 == 0) qsc[c] = __uint_as_float((eb - 7u) << 23);  // columns behind the rows too: their scores of 0 stay 0
-  }
-}
 
 // Adds 32 columns' weights of one key to sum.  ALL: every column collects, so
 // that some exponentials may leave the MUFU unit (the polynomial has no zero
@@ -406,7 +349,9 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const float* qsc = reinterpret_cast<float*>(smem + SM::QSC) + (seg & 1) * QR;
       if (KV8) {  // both tile parities' warps write the queries, when the last segment's products are done
         if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 945)) break;
-        weights_split_q(wp, smem, SM::QHALF, const_cast<float*>(qsc), w.g, w.row0 + w.m * p.R, rows, warp - 4);
+        uint4 raw[QR / 32];
+        load_queries<QR / 32, 16>(p, w.g, w.row0 + w.m * p.R, rows, warp - 4, raw);
+        split_queries<QR / 32, 16, 1>(raw, smem, SM::QHALF, const_cast<float*>(qsc), rows, warp - 4);
         fence_proxy_async_smem();
       }
       __syncwarp();

@@ -119,6 +119,8 @@ TreeParams tree_params(const hs2_cache* c, const hs2_draft* d, int rows) {
   p.cu = d->cu_draft;
   p.ctx = d->ctx_len;
   p.mask = d->mask;
+  p.q_tok = d->q_tok_stride;
+  p.q_head = d->q_head_stride;
   p.scale_log2 = scale_log2(HD);
   p.ksc = c->k_scale;
   p.vsc = c->v_scale;
@@ -447,8 +449,7 @@ int hs2_tree_attn(const hs2_cache* cache, const hs2_draft* draft, const void* q,
   const int rb = most <= 32 ? 32 : 128;
   TreeParams p = tree_params(cache, draft, rb);
   p.o = static_cast<__nv_bfloat16*>(o);
-  p.o_tok = draft->q_tok_stride;
-  p.o_head = draft->q_head_stride;
+  p.q = static_cast<const __nv_bfloat16*>(q);
   p.lse = lse;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.part_o = reinterpret_cast<float*>(w);
@@ -457,7 +458,8 @@ int hs2_tree_attn(const hs2_cache* cache, const hs2_draft* draft, const void* q,
   CUtensorMap mq, mk, mv;
   if (int rc = make_map(&mq, q, draft->n_tok, draft->Hq, draft->q_tok_stride, draft->q_head_stride, p.G, p.R))
     return rc;
-  if (int rc = make_pool_map(&mk, cache, cache->k)) return rc;
+  // blocks of 32 rows take K's codes as they are, a full block converts them
+  if (int rc = make_pool_map(&mk, cache, cache->k, rb == 32)) return rc;
   if (int rc = make_pool_map(&mv, cache, cache->v)) return rc;
   const Range range("hs2 tree_attn");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -485,9 +487,7 @@ int hs2_cache_weights(const hs2_cache* cache, const hs2_draft* draft, const void
   p.acc = acc;
   p.acc_stride = acc_stride;
   p.t.max_len = std::min(p.t.max_len, acc_stride);
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_tok = draft->q_tok_stride;
-  p.q_head = draft->q_head_stride;
+  p.t.q = static_cast<const __nv_bfloat16*>(q);
   CUtensorMap mq, mk;
   if (int rc = make_map(&mq, q, draft->n_tok, draft->Hq, draft->q_tok_stride, draft->q_head_stride, p.t.G, p.t.R))
     return rc;

@@ -25,16 +25,21 @@
 //   few rows a tile's 128 rows are 4 blocks of 32, copies of the unit's
 //            rows where those fit, and block k keeps only its share of the
 //            tile's keys (the rest of its P is zero): all warps share one row's
-//            exponentials, instead of one warp taking all of them (T = 1, e4m3
-//            cache of 4 x 32768 tokens 121 -> 107 us; bf16 64 short sequences
-//            36 -> 32.5 us, one of 2048 tokens 14 -> 13). Each block is a
+//            exponentials, instead of one warp taking all of them (bf16, 64
+//            short sequences 36 -> 32.5 us, one of 2048 tokens 14 -> 13; e4m3
+//            with the codes as below 121 -> 92 us). Each block is a
 //            softmax of its own; the epilogue adds the blocks' O, each block a
 //            share of the columns;
-//   e4m3     codes arrive by TMA in a raw ring; eight warps turn them into bf16
-//            (exact; unlike f16 it leaves Q and P their whole range), another
-//            fetches the scales; the K scale multiplies the scores, the V
-//            scale multiplies P before its rounding. Bound by that softmax and
-//            the conversion, not by memory: 2.4 TB/s at 128 rows, 2.6 at 8;
+//   e4m3     codes arrive by TMA; eight warps turn them into bf16 (exact; unlike
+//            f16 it leaves Q and P their whole range), another fetches the
+//            scales; the K scale multiplies the scores, the V scale multiplies
+//            P before its rounding.  Few rows: K's codes are the products'
+//            operand as they are, the queries pairs of e4m3 rows
+//            (split_queries), and only V is converted (4 x 32768 tokens, T = 1:
+//            107 -> 92 us); for a full block the split of 128 rows costs more
+//            than it saves (64 short sequences, T = 6: 52 us, 62 with it).
+//            Bound by the conversion and the softmax with its scales, not by
+//            memory: 2.4 TB/s at 128 rows, 3.0 at 8;
 //   edges    columns without a visible key become -inf whatever they hold, V
 //            rows behind the last key are zeroed before the product.
 #pragma once
@@ -42,11 +47,12 @@
 #include <cuda_fp16.h>
 
 #include "attn_tile.cuh"
+#include "quantize.cuh"
 
 namespace hs2 {
 
 constexpr int TR_MAX_ITEMS = 6;  // tiles of 32 KB in the ring, at most
-constexpr int TR_MAX_RAW = 5;    // e4m3: raw tiles of 16 KB, at most
+constexpr int TR_MAX_RAW = 5;    // e4m3: tiles of codes, 16 KB, in a ring, at most
 constexpr int TR_OVERHEAD = 3;   // what a unit costs beside its key tiles, in tiles (see tree_split)
 constexpr int TR_SCALES = 8;     // e4m3: key tiles whose scales are held or on their way
 constexpr uint32_t RAW_BYTES = 128u * 128u;
@@ -61,8 +67,9 @@ struct TreeParams {
   const uint64_t* mask;
   float scale_log2;
   const float *ksc, *vsc;  // e4m3 only
+  const __nv_bfloat16* q;  // where the queries are split (else by TMA)
+  int64_t q_tok, q_head;   // of q and o
   __nv_bfloat16* o;
-  int64_t o_tok, o_head;
   float* lse;
   float* part_o;    // [CTA][2][128][128], un-normalised
   float2* part_ml;  // [CTA][2][128]
@@ -73,9 +80,10 @@ struct TreeParams {
 
 struct TreeBars {
   uint64_t full[TR_MAX_ITEMS], empty[TR_MAX_ITEMS];
-  uint64_t raw_full[TR_MAX_RAW], raw_empty[TR_MAX_RAW];
+  uint64_t k8_full[TR_MAX_RAW], k8_empty[TR_MAX_RAW], v8_full[2], v8_empty[2];  // e4m3
   uint64_t sc_full[TR_SCALES], sc_empty[TR_SCALES];
   uint64_t q_full, q_empty;
+  uint64_t qsc_read;  // few rows, e4m3: every softmax warp has a segment's row scales (and has seen q_full's phase)
   uint64_t v_raw[TR_MAX_ITEMS];  // a V tile landed whose rows behind the sequence are not yet zeroed
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t ml_ready, o_free;
@@ -88,23 +96,26 @@ struct TreeBars {
   uint32_t tmem_slot;
   int abort;
 };
-constexpr uint32_t TR_BAR_BYTES = 640;
+constexpr uint32_t TR_BAR_BYTES = 704;
 static_assert(sizeof(TreeBars) <= TR_BAR_BYTES, "barrier area");
 
 // RB: rows of a block (32 or 128); a unit has RB / G tokens.
 template <bool KV8, int RB>
 struct TreeSmem {
   static constexpr int BLOCKS = 128 / RB;
-  static constexpr int ITEMS = KV8 ? 3 : BLOCKS > 1 ? 5 : 6;
-  static constexpr int RAWS = BLOCKS > 1 ? 4 : 5;
-  static_assert(ITEMS <= TR_MAX_ITEMS && RAWS <= TR_MAX_RAW, "rings");
+  static constexpr bool CODES = KV8 && BLOCKS > 1;  // K's codes are the products' operand
+  static constexpr int ITEMS = CODES ? 2 : KV8 ? 3 : BLOCKS > 1 ? 5 : 6;  // CODES: V tiles only
+  static constexpr int K8 = CODES ? 3 : 5, V8 = CODES ? 2 : 0;  // rings of codes; else K's and V's in one
+  static_assert(ITEMS <= TR_MAX_ITEMS && K8 <= TR_MAX_RAW && V8 <= TR_MAX_RAW, "rings");
   static constexpr uint32_t ITEM = TILE_BYTES;  // after Q
-  static constexpr uint32_t RAW = ITEM + ITEMS * TILE_BYTES;
-  static constexpr uint32_t SCALE = RAW + (KV8 ? RAWS * RAW_BYTES : 0u);
+  static constexpr uint32_t K8_AT = ITEM + ITEMS * TILE_BYTES;
+  static constexpr uint32_t V8_AT = K8_AT + (KV8 ? K8 * RAW_BYTES : 0u);
+  static constexpr uint32_t SCALE = V8_AT + V8 * RAW_BYTES;
   static constexpr uint32_t BAR = SCALE + (KV8 ? TR_SCALES * 1024u : 0u);
   static constexpr uint32_t ML = BAR + TR_BAR_BYTES;     // float2 [2][128]
   static constexpr uint32_t EXCH = ML + 2048u;   // float [2][128 - RB][32]
-  static constexpr uint32_t BYTES = EXCH + 2u * (128 - RB) * 128u;
+  static constexpr uint32_t QSC = EXCH + 2u * (128 - RB) * 128u;  // CODES: float [RB], what a row's scores are times
+  static constexpr uint32_t BYTES = QSC + (CODES ? RB * 4u : 0u);
   static_assert(BYTES <= 232448u, "shared memory of one CTA");
 };
 
@@ -337,12 +348,72 @@ __device__ __forceinline__ void convert_tile(uint32_t raw_tile, uint32_t tile, i
   }
 }
 
+// Query rows of a tile, 16 bytes a lane and step: WARPS warps (w) take 2 rows each
+// a step, rows [0, rows) exist, those behind them are zeros.
+template <int STEPS, int WARPS>
+__device__ __forceinline__ void load_queries(const TreeParams& p, int g, int64_t row0, int rows, int w,
+                                             uint4 (&raw)[STEPS]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int c = 2 * WARPS * s + 2 * w + (lane >> 4);
+    raw[s] = make_uint4(0, 0, 0, 0);
+    if (c < rows)
+      raw[s] = *reinterpret_cast<const uint4*>(p.q + (row0 + c / p.G) * p.q_tok + (g * p.G + c % p.G) * p.q_head +
+                                               8 * (lane & 15));
+  }
+}
+
+// Those rows as pairs of e4m3 rows (K-major, 128-byte swizzle, the second part
+// `half` bytes behind): a bf16 value has 8 significant bits, two e4m3 values of
+// 4 hold it where it is not below 2^-9 of its row's maximum (then the error is
+// at most 2^-18 of that maximum).  A row is scaled by the power of two that
+// brings its maximum to [128, 256); qsc gets the inverse.  Steps that begin at
+// `upto` or behind are left out; COPIES copies of the tile are written.
+template <int STEPS, int WARPS, int COPIES>
+__device__ __forceinline__ void split_queries(const uint4 (&raw)[STEPS], uint8_t* smem, uint32_t half, float* qsc,
+                                              int upto, int w) {
+  const int lane = threadIdx.x & 31, l16 = lane & 15;
+  constexpr int STEP = 2 * WARPS;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    if (STEP * s >= upto) break;
+    const int c = STEP * s + 2 * w + (lane >> 4);
+    const uint32_t v[4] = {raw[s].x, raw[s].y, raw[s].z, raw[s].w};
+    uint32_t top = 0;  // the exponents' maximum, in bits 7 .. 14
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7f80u, (v[e] >> 16) & 0x7f80u));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t eb = max(top >> 7, 8u);
+    const float up = __uint_as_float(min(261u - eb, 254u) << 23);
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = __uint_as_float(v[e] << 16) * up, y = __uint_as_float(v[e] & 0xffff0000u) * up;
+      const uint32_t a = e4m3x2_from_f32(x, y), h = e4m3x2_to_f16x2(a);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      const uint32_t b = e4m3x2_from_f32(x - f.x, y - f.y);
+      hi[e >> 1] = (e & 1) ? hi[e >> 1] | a << 16 : a;
+      lo[e >> 1] = (e & 1) ? lo[e >> 1] | b << 16 : b;
+    }
+#pragma unroll
+    for (int k = 0; k < COPIES; ++k) {
+      uint8_t* dst = smem + k * STEPS * STEP * 128 + sw128_chunk_offset(c, l16 >> 1, 0) + 8 * (l16 & 1);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + half) = make_uint2(lo[0], lo[1]);
+    }
+    if (l16 == 0) qsc[c] = __uint_as_float((eb - 7u) << 23);
+  }
+}
+
 template <bool KV8, int RB>
 __global__ void __launch_bounds__(tr_threads(KV8), 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const TreeParams p) {
   using SM = TreeSmem<KV8, RB>;
-  constexpr int ITEMS = SM::ITEMS, RAWS = SM::RAWS, BLOCKS = SM::BLOCKS;
+  constexpr int ITEMS = SM::ITEMS, K8 = SM::K8, V8 = SM::V8, BLOCKS = SM::BLOCKS;
+  constexpr bool CODES = SM::CODES;
   extern __shared__ __align__(1024) uint8_t tree_smem[];
   uint8_t* smem = tree_smem;
   TreeBars* bars = reinterpret_cast<TreeBars*>(smem + SM::BAR);
@@ -373,17 +444,22 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         mbar_init(&bars->v_raw[s], 1);
       }
       if (KV8) {
-        for (int s = 0; s < RAWS; ++s) {
-          mbar_init(&bars->raw_full[s], 1);
-          mbar_init(&bars->raw_empty[s], TR_CONV / 32);
+        for (int s = 0; s < K8; ++s) {
+          mbar_init(&bars->k8_full[s], 1);
+          mbar_init(&bars->k8_empty[s], CODES ? 1 : TR_CONV / 32);
+        }
+        for (int s = 0; s < V8; ++s) {
+          mbar_init(&bars->v8_full[s], 1);
+          mbar_init(&bars->v8_empty[s], TR_CONV / 32);
         }
         for (int s = 0; s < TR_SCALES; ++s) {
           mbar_init(&bars->sc_full[s], 32);
           mbar_init(&bars->sc_empty[s], 4);
         }
       }
-      mbar_init(&bars->q_full, 1);
+      mbar_init(&bars->q_full, CODES ? TR_CONV / 32 : 1);
       mbar_init(&bars->q_empty, 1);
+      mbar_init(&bars->qsc_read, 8);
       for (int x = 0; x < 2; ++x) {
         mbar_init(&bars->s_full[x], 1);
         mbar_init(&bars->p_ready[x], 4);
@@ -446,6 +522,13 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         bits = p.mask ? p.mask[w.row0 + t] : (2ull << t) - 1;  // t = 63: 2 << 63 = 0, minus 1: all
         if (w.T < 64) bits &= (1ull << w.T) - 1;
       }
+      float scale = p.scale_log2;
+      if (CODES) {
+        if (!(ok = warp_wait(&bars->q_full, seg & 1, p.limit_ns, abort_flag, 847))) break;
+        scale *= reinterpret_cast<const float*>(smem + SM::QSC)[row_r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->qsc_read);
+      }
       RowState st;
       for (int j = x; j < n; j += 2, ++ns) {
         if (!(ok = warp_wait(&bars->s_full[x], ns & 1, p.limit_ns, abort_flag, 841))) break;
@@ -465,9 +548,9 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           bool resc;
           if (base + 128 > w.ctx) {
             tree_visible(w.ctx, base, bits, vis);
-            resc = softmax_quarters<RB / 32, KV8, true>(s_tm, q0, p.scale_log2, sc_s, vs_s, vis, st, alpha);
+            resc = softmax_quarters<RB / 32, KV8, true>(s_tm, q0, scale, sc_s, vs_s, vis, st, alpha);
           } else {
-            resc = softmax_quarters<RB / 32, KV8, false>(s_tm, q0, p.scale_log2, sc_s, vs_s, vis, st, alpha);
+            resc = softmax_quarters<RB / 32, KV8, false>(s_tm, q0, scale, sc_s, vs_s, vis, st, alpha);
           }
           // P V(j - 2) completed before S(j): s_full's commit covers it
           if (j >= 2 && __any_sync(0xffffffffu, resc)) rescale_row(o_tm + 128 * x, alpha);
@@ -589,7 +672,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         if (!warp_live || !row_live) continue;
         const int col = c * 32 + block * SHARE;  // SHARE columns from here on, in v
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + col);
+          uint4* dst = reinterpret_cast<uint4*>(p.o + row * p.q_tok + static_cast<int64_t>(h) * p.q_head + col);
 #pragma unroll
           for (int q = 0; q < SHARE / 8; ++q) {
             uint32_t o[4];
@@ -635,13 +718,8 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       // =========================================================== TMA loads
       TreeWalk w;
       const bool work = !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars);
-      constexpr int RING = KV8 ? RAWS : ITEMS;
-      constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
-      uint64_t* full = KV8 ? bars->raw_full : bars->full;
-      uint64_t* empty = KV8 ? bars->raw_empty : bars->empty;
-      uint8_t* ring = smem + (KV8 ? SM::RAW : SM::ITEM);
       const int page = 1 << p.page_log2, per_tile = 128 >> p.page_log2;
-      int item = 0;
+      int item = 0, kc = 0, vc = 0;  // in one ring, or (CODES) K and V in rings of their own
       uint32_t raw_used = 0, raw_uses = 0;  // slots last filled through v_raw, and how often (mod 2)
       bool ok = work;
       while (ok) {
@@ -661,8 +739,12 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           bool is_v;
           tree_item(u, n, tile, is_v);
           const int next_pg = page_of(u + 1);
-          const int slot = item % RING;
-          if (item >= RING && !warp_wait(&empty[slot], ((item / RING) - 1) & 1, p.limit_ns, abort_flag, 812)) {
+          const bool v8 = CODES && is_v;
+          const int ring = !KV8 ? ITEMS : v8 ? V8 : K8, at = !CODES ? item : is_v ? vc : kc;
+          const int slot = at % ring;
+          uint64_t* full = !KV8 ? bars->full : v8 ? bars->v8_full : bars->k8_full;
+          uint64_t* empty = !KV8 ? bars->empty : v8 ? bars->v8_empty : bars->k8_empty;
+          if (at >= ring && !warp_wait(&empty[slot], ((at / ring) - 1) & 1, p.limit_ns, abort_flag, 812)) {
             ok = false;
             break;
           }
@@ -682,52 +764,61 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
               pg = p.n_pages;  // behind the pools: reads as zeros
             }
             const CUtensorMap* map = is_v ? &tmV : &tmK;
-            uint8_t* dst = ring + slot * SLOT + lane * page * 128;
+            uint8_t* dst = smem + lane * page * 128 +
+                           (!KV8 ? SM::ITEM + slot * TILE_BYTES : (v8 ? SM::V8_AT : SM::K8_AT) + slot * RAW_BYTES);
             const int tok = pg << p.page_log2;
             tma_load_3d(dst, map, bar, 0, w.g, tok);
             if (!KV8) tma_load_3d(dst + HALF_BYTES, map, bar, 64, w.g, tok);
           }
+          (is_v ? vc : kc) += 1;
           pg = next_pg;
         }
         if (!ok || !w.next(p)) break;
       }
       // never leave a TMA write in flight into memory the CTA gives back
       __syncwarp();
-      if (lane == 0 && work)
-        for (int u = max(0, item - RING); u < item; ++u)
-          if (raw_used >> (u % RING) & 1u)
-            wait_done(&bars->v_raw[u % RING], ~(raw_uses >> (u % RING)) & 1u, p.limit_ns, 817);
+      if (lane == 0 && work && KV8) {
+        const int in_k8 = CODES ? kc : item;
+        for (int u = max(0, in_k8 - K8); u < in_k8; ++u)
+          wait_done(&bars->k8_full[u % K8], (u / K8) & 1, p.limit_ns, 814);
+        if constexpr (CODES)
+          for (int u = max(0, vc - V8); u < vc; ++u) wait_done(&bars->v8_full[u % V8], (u / V8) & 1, p.limit_ns, 817);
+      } else if (lane == 0 && work) {
+        for (int u = max(0, item - ITEMS); u < item; ++u)
+          if (raw_used >> (u % ITEMS) & 1u)
+            wait_done(&bars->v_raw[u % ITEMS], ~(raw_uses >> (u % ITEMS)) & 1u, p.limit_ns, 817);
           else
-            wait_done(&full[u % RING], (u / RING) & 1, p.limit_ns, 814);
+            wait_done(&bars->full[u % ITEMS], (u / ITEMS) & 1, p.limit_ns, 814);
+      }
     } else if (warp == 1) {
       // ========================================================== MMA issue
       TreeWalk w;
       if (w.begin(p, bars)) {  // the warp walks together, its elected lane issues
-        int item = 0, seg = 0;
+        int item = 0, vc = 0, seg = 0;  // next item, or (CODES) K tile, next V tile
         uint32_t np = 0;  // by tile parity: tiles so far (mod 2)
         bool ok = true;
-        // One lane polls for few rows of an e4m3 cache (4 x 32768 tokens, T = 1: 107
-        // us, all lanes 119), all do otherwise (4 x 131072, T = 16: 331 us, one
-        // lane 344).
         auto wait_for = [&](uint64_t* bar, uint32_t parity, int where) {
-          if constexpr (!KV8 || BLOCKS == 1) return warp_wait(bar, parity, p.limit_ns, abort_flag, where);
-          const bool mine = lane != 0 || mbar_wait(bar, parity, p.limit_ns, abort_flag, where);
-          return __all_sync(0xffffffffu, mine) != 0;
+          return warp_wait(bar, parity, p.limit_ns, abort_flag, where);
         };
-        auto wait_item = [&](int u) {
+        auto wait_item = [&](int u) {  // (CODES) of K only
+          if constexpr (CODES) return wait_for(&bars->k8_full[u % K8], (u / K8) & 1, 821);
           return wait_for(&bars->full[u % ITEMS], (u / ITEMS) & 1, 821);
         };
         auto issue_s = [&](int x, int u, bool last) {
           const uint64_t da = sdesc_sw128(q_base, 16, 1024);
-          const uint64_t db = sdesc_sw128(item_base + (u % ITEMS) * TILE_BYTES, 16, 1024);
+          const uint64_t db = sdesc_sw128(CODES ? smem_u32(smem + SM::K8_AT) + (u % K8) * RAW_BYTES
+                                                : item_base + (u % ITEMS) * TILE_BYTES, 16, 1024);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const uint32_t koff = ((kk >> 2) * HALF_BYTES + (kk & 3) * 32) >> 4;
-              umma_ss(tmem + x * 128, da + koff, db + koff, IDESC_S, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 8; ++kk) {  // CODES: the same keys times both parts of the queries
+              const uint32_t step = (kk & 3) * 32 >> 4, second = (kk >> 2) * HALF_BYTES >> 4;
+              if (CODES)
+                umma_ss_f8(tmem + x * 128, da + second + step, db + step, idesc_e4m3_f32(128, 128), kk > 0 ? 1u : 0u);
+              else
+                umma_ss(tmem + x * 128, da + second + step, db + second + step, IDESC_S, kk > 0 ? 1u : 0u);
             }
             umma_commit(&bars->s_full[x]);
-            umma_commit(&bars->empty[u % ITEMS]);
+            umma_commit(CODES ? &bars->k8_empty[u % K8] : &bars->empty[u % ITEMS]);
             if (last) umma_commit(&bars->q_empty);
           }
           __syncwarp();
@@ -757,19 +848,22 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           }
           for (int j = 0; j < n; ++j) {
             const int x = j & 1;
-            // a bf16 V(j) and K(j + 2) normally landed long ago: nothing but P
-            // stands between its arrival and the products.  Of an e4m3 cache
-            // K(j + 2) may still be converted, so P V does not wait for it.
-            ok = wait_item(item) && (KV8 || j + 2 >= n || wait_item(item + 1));
+            // V(j) and K(j + 2) normally landed long ago: nothing but P stands
+            // between its arrival and the products.  A K(j + 2) that is converted
+            // may not be there yet, so P V does not wait for it.
+            if constexpr (CODES)
+              ok = wait_for(&bars->full[vc % ITEMS], (vc / ITEMS) & 1, 827) && (j + 2 >= n || wait_item(item));
+            else
+              ok = wait_item(item) && (KV8 || j + 2 >= n || wait_item(item + 1));
             // the last segment's O has been read
             if (ok && j == 0 && seg > 0) ok = wait_for(&bars->o_free, (seg - 1) & 1, 824);
             if (ok) ok = wait_for(&bars->p_ready[x], (np >> x) & 1, 825);
             np ^= 1u << x;
             if (!ok) break;
             tc_fence_after();
-            issue_pv(x, item++, j < 2, j + 2 >= n);
+            issue_pv(x, CODES ? vc++ : item++, j < 2, j + 2 >= n);
             if (j + 2 < n) {
-              if (KV8) {
+              if (KV8 && !CODES) {
                 if (!(ok = wait_item(item))) break;
                 tc_fence_after();
               }
@@ -787,7 +881,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       // ======================= a segment's queries, once the last one's products
       // have read theirs (the K / V loads above do not wait for that)
       TreeWalk w;
-      if (lane == 0 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
+      if (!CODES && lane == 0 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
         const uint32_t half = static_cast<uint32_t>(p.R * p.G) * 128u;
         int seg = 0;
         do {
@@ -862,30 +956,49 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
         }
       }
     } else {
-      // ================================================== e4m3: codes to bf16
+      // ==== e4m3: codes to bf16, K's and V's or (CODES) V's, and a segment's queries
+      // to pairs of codes
       TreeWalk w;
       if (KV8 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
         const int pt = threadIdx.x - 384;
-        const uint32_t raw_base = smem_u32(smem + SM::RAW);
-        int item = 0;
+        const uint32_t raw_base = smem_u32(smem + (CODES ? SM::V8_AT : SM::K8_AT));
+        constexpr int RAWS = CODES ? V8 : K8;
+        uint64_t* raw_full = CODES ? bars->v8_full : bars->k8_full;
+        uint64_t* raw_empty = CODES ? bars->v8_empty : bars->k8_empty;
+        int at = 0, seg = 0;
         bool ok = true;
         do {
+          if constexpr (CODES) {
+            constexpr int STEPS = RB * 32 / (2 * TR_CONV);
+            uint4 raw[STEPS];
+            load_queries<STEPS, TR_CONV / 32>(p, w.g, w.row0 + w.m * p.R, w.rows(p), pt >> 5, raw);
+            // the last segment's products have read its queries, the softmax its scales
+            if (seg > 0 && !(warp_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 816) &&
+                             warp_wait(&bars->qsc_read, (seg - 1) & 1, p.limit_ns, abort_flag, 818)))
+              break;
+            split_queries<STEPS, TR_CONV / 32, BLOCKS>(raw, smem, HALF_BYTES, reinterpret_cast<float*>(smem + SM::QSC),
+                                                       RB, pt >> 5);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->q_full);
+            ++seg;
+          }
           const int n = w.n(), len = w.ctx + w.T;
-          for (int u = 0; u < 2 * n && ok; ++u, ++item) {
-            int tile;
-            bool is_v;
-            tree_item(u, n, tile, is_v);
+          for (int u = 0; u < (CODES ? n : 2 * n) && ok; ++u, ++at) {
+            int tile = u;
+            bool is_v = true;
+            if (!CODES) tree_item(u, n, tile, is_v);
             const int keys = len - (w.t0 + tile) * 128;  // rows from here on are behind the sequence
-            const int rs = item % RAWS, cs = item % ITEMS;
-            ok = warp_wait(&bars->raw_full[rs], (item / RAWS) & 1, p.limit_ns, abort_flag, 851) &&
-                 (item < ITEMS || warp_wait(&bars->empty[cs], ((item / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 852));
+            const int rs = at % RAWS, cs = at % ITEMS;
+            ok = warp_wait(&raw_full[rs], (at / RAWS) & 1, p.limit_ns, abort_flag, 851) &&
+                 (at < ITEMS || warp_wait(&bars->empty[cs], ((at / ITEMS) - 1) & 1, p.limit_ns, abort_flag, 852));
             if (!ok) break;
             convert_tile<TR_CONV>(raw_base + rs * RAW_BYTES, item_base + cs * TILE_BYTES, keys, pt);
             fence_proxy_async_smem();
             __syncwarp();  // one arrival per warp: 256 of them would take longer than the conversion
             if (lane == 0) {
               mbar_arrive(&bars->full[cs]);
-              mbar_arrive(&bars->raw_empty[rs]);
+              mbar_arrive(&raw_empty[rs]);
             }
           }
         } while (ok && w.next(p));
@@ -963,7 +1076,7 @@ __global__ void __launch_bounds__(32 * TM_WARPS) tree_merge_kernel(const TreePar
       const float inv = L == 0.f ? 0.f : 1.f / L;
       const int h = u.z * p.G + r % p.G;
       const int64_t row = u.x + r / p.G;
-      *reinterpret_cast<uint2*>(p.o + row * p.o_tok + static_cast<int64_t>(h) * p.o_head + lane * 4) =
+      *reinterpret_cast<uint2*>(p.o + row * p.q_tok + static_cast<int64_t>(h) * p.q_head + lane * 4) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (lane == 0 && p.lse)
         p.lse[static_cast<int64_t>(h) * p.n_tok + row] = (M + log2f(L)) * 0.69314718055994530942f;
