@@ -209,6 +209,34 @@ def test_without_lse_and_an_e4m3_cache_with_strides():
                           rtol=3e-4)                                   # every row of a group sums to one
 
 
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("drafts", [3, 20])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(bad, drafts, kv8):
+    c = Paged([300, 41], [drafts, 2], 8, 2, kv8, 64, True, seed=40)
+    ref, rl, spread = c.oracle()
+    c.q[1, 5, 7] = bad
+    c.device(DEV)
+    o, lse, gb = _attend(c)
+    hs2.hs2_sync()
+    got, keep = f64(o), np.ones(ref.shape[:2], bool)
+    keep[1, 5] = False
+    assert np.isnan(got[1, 5]).all() and torch.isnan(lse[5, 1])
+    check_o(got[keep], ref[keep], spread[keep])
+
+
+def test_rows_of_very_different_size():
+    """Each query row has a scale of its own: large and small rows, zeros, numbers far below their row's largest."""
+    c = Paged([260, 77], [3, 4], 8, 2, True, 64, True, seed=41)
+    f = torch.tensor([2.0 ** -100, 2.0 ** -20, 1e-3, 1.0, 3.0, 0.0, 0.5])
+    c.q = (c.q.float() * f[:, None, None]).to(torch.bfloat16)
+    c.q[3, :, ::2] *= 2.0 ** -12
+    c.device(DEV)
+    o, lse, gb = _attend(c)
+    rl = _check(c, o, lse, gb)
+    _weights(c, rl)
+
+
 def test_more_drafts_than_said_are_reported():
     c = Paged([130, 61], [3, 5], 8, 2, False, 64, True, seed=17).device(DEV)
     ref, rl, spread = c.oracle()

@@ -368,7 +368,8 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, int g, int64_t
 // `half` bytes behind): a bf16 value has 8 significant bits, two e4m3 values of
 // 4 hold it where it is not below 2^-9 of its row's maximum (then the error is
 // at most 2^-18 of that maximum).  A row is scaled by the power of two that
-// brings its maximum to [128, 256); qsc gets the inverse.  Steps that begin at
+// brings its maximum to [128, 256), or less for a row of zeros or nearly so;
+// qsc gets the inverse.  Steps that begin at
 // `upto` or behind are left out; COPIES copies of the tile are written.
 template <int STEPS, int WARPS, int COPIES>
 __device__ __forceinline__ void split_queries(const uint4 (&raw)[STEPS], uint8_t* smem, uint32_t half, float* qsc,
@@ -385,8 +386,10 @@ __device__ __forceinline__ void split_queries(const uint4 (&raw)[STEPS], uint8_t
     for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7f80u, (v[e] >> 16) & 0x7f80u));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const uint32_t eb = max(top >> 7, 8u);
-    const float up = __uint_as_float(min(261u - eb, 254u) << 23);
+    // not below 2^-111: the inverse times log2(e) / sqrt(d) has to stay a normal
+    // number (as a subnormal it became 0, and 0 times a masked key's -inf a NaN)
+    const uint32_t eb = max(top >> 7, 16u);
+    const float up = __uint_as_float((261u - eb) << 23);
     uint32_t hi[2], lo[2];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -403,7 +406,8 @@ __device__ __forceinline__ void split_queries(const uint4 (&raw)[STEPS], uint8_t
       *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(dst + half) = make_uint2(lo[0], lo[1]);
     }
-    if (l16 == 0) qsc[c] = __uint_as_float((eb - 7u) << 23);
+    // the codes saturate: a row with an infinity or a NaN is made NaN by its scale
+    if (l16 == 0) qsc[c] = __uint_as_float(eb == 255u ? 0x7fffffffu : (eb - 7u) << 23);
   }
 }
 
