@@ -150,3 +150,67 @@ def test_prompt_draft_accept_evict_decode(kv8):
     left = new_len.tolist()
     hs2.hs2_qk_norm_rope(cache, q, k, v, wq, wk, 1e-6, freq, i32(lens), slots(left, [1] * B), q1)
     attend(q1, list(range(B + 1)), left, None, "after the cut")
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_a_captured_decode_step_equals_eager_ones(kv8):
+    """Rotation, attention and weights of one token a sequence as one graph, replayed over advancing lengths: bit for
+    bit what the calls give one by one, on another stream and over pools of their own."""
+    Hq, Hkv, page, max_pages, steps = 16, 2, 64, 8, 6
+    lens = [0, 1, 62, 127, 300]
+    B = len(lens)
+    g = torch.Generator().manual_seed(22)
+    table = torch.randperm(B * max_pages, generator=g).view(B, max_pages).to(torch.int32)
+    freq = torch.from_numpy(1e4 ** (-np.arange(64) / 64)).to(DEV)
+    shape = (B * max_pages * page, Hkv, 128)
+    start = [torch.randn(shape, generator=g).to(torch.bfloat16) for _ in range(2)]
+    rows = torch.randn((steps, B, Hq + 2 * Hkv, 128), generator=g).to(torch.bfloat16).to(DEV)
+
+    def state():
+        s = dict(ks=None, vs=None)
+        if kv8:
+            (s["k"], s["ks"]), (s["v"], s["vs"]) = ([t.to(DEV) for t in inputs.quantize_e4m3(x)] for x in start)
+        else:
+            s["k"], s["v"] = (x.to(DEV) for x in start)
+        s["cache"] = hs2.make_cache(s["k"], s["v"], table.to(DEV), page, s["ks"], s["vs"])
+        s["acc"] = torch.zeros((B, Hkv, max_pages * page), device=DEV)
+        s["x"] = torch.zeros((B, Hq + 2 * Hkv, 128), dtype=torch.bfloat16, device=DEV)
+        s["q"], s["o"] = (torch.zeros((B, Hq, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        s["lse"] = torch.zeros((Hq, B), device=DEV)
+        s["ctx"], s["slots"] = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+        s["draft"] = hs2.make_draft(s["q"], torch.arange(B + 1, dtype=torch.int32, device=DEV), s["ctx"], None, 1)
+        s["ws"] = torch.empty(hs2.tree_attn_workspace_bytes(s["cache"], s["draft"]), dtype=torch.uint8, device=DEV)
+        return s
+
+    def set_step(s, i):
+        at = [n + i for n in lens]
+        s["x"].copy_(rows[i])
+        s["ctx"].copy_(torch.tensor(at, dtype=torch.int32))
+        s["slots"].copy_(torch.tensor([int(table[b, n // page]) * page + n % page for b, n in enumerate(at)],
+                                      dtype=torch.int32))
+
+    def step(s, stream=None):
+        q, k, v = s["x"].split((Hq, Hkv, Hkv), 1)
+        hs2.hs2_qk_norm_rope(s["cache"], q, k, v, None, None, 0.0, freq, s["ctx"], s["slots"], s["q"], stream=stream)
+        hs2.hs2_tree_attn(s["cache"], s["draft"], s["q"], s["o"], s["lse"], s["ws"], stream)
+        hs2.hs2_cache_weights(s["cache"], s["draft"], s["q"], s["lse"], None, s["acc"], stream)
+
+    eager, captured = state(), state()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(captured)
+    side = torch.cuda.Stream()
+    for i in range(steps):
+        set_step(captured, i)
+        set_step(eager, i)
+        torch.cuda.synchronize()
+        graph.replay()
+        step(eager, side)
+        torch.cuda.synchronize()
+        hs2.hs2_sync()
+        for n in ("q", "o", "lse", "acc", "k", "v", "ks", "vs"):
+            if eager[n] is not None:
+                assert torch.equal(eager[n].view(torch.uint8), captured[n].view(torch.uint8)), (i, n)
+    total = captured["acc"].sum(-1).cpu()
+    assert torch.allclose(total, torch.full((B, Hkv), steps * Hq / Hkv), rtol=3e-4)  # a row's weights sum to one

@@ -20,16 +20,16 @@
 // A query row times a power of two is the sum of two e4m3 rows (split_queries),
 // so eight products of 32 give the scores that eight of 16 give in bf16; the
 // key's scale and the row's power of two multiply them afterwards.  Turning the
-// codes into bf16 instead took 245 us for 4 x 131072 tokens and 128 rows, where
-// this takes 188.
+// codes into bf16 instead took 245 us for 32 tokens (256 rows) over 2 sequences
+// of up to 131072, where this takes 188.
 //
 // Bound by memory at few rows (4 x 32768 tokens of 64/8 heads, 8 rows: bf16 50
 // us, 5.5 TB/s; e4m3 44 us, 3.3 TB/s, there the steps of a tile are longer than
-// its load), then by the exponentials (512 rows: 187 and 223 us): 16 a clock and
-// SM on the MUFU unit, so where all 32 columns of a chunk count four
-// of its sixteen pairs take the degree-4 polynomial on the FMA pipes instead
-// (2.6e-6; the cubic that kernel (2) mixes in is exact only to 7.5e-5; none of
-// them 199 and 235 us, eight 202 and 257).
+// its load), then by the sums (512 rows: 187 and 223 us), of which the
+// exponentials are a large part: 16 a clock and SM on the MUFU unit, so where all
+// 32 columns of a chunk count four of its sixteen pairs take the degree-4
+// polynomial on the FMA pipes instead (2.6e-6; the cubic that kernel (2) mixes in
+// is exact only to 7.5e-5; none of them 199 and 235 us, eight 202 and 257).
 #pragma once
 
 #include "tree_attn.cuh"

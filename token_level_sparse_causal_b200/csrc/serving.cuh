@@ -349,7 +349,7 @@ int hs2_cache_evict(const hs2_cache* cache, const int32_t* seq_len, const float*
   p.idx = idx;
   p.new_len = new_len;
   // CTAs a row: as many as let every row run at once, up to a portable cluster
-  // (16 rows of 131072 positions: two waves of clusters of 8 take 80 us, one of
+  // (16 rows of up to 131072 positions: two waves of clusters of 8 take 80 us, one of
   // clusters of 6 53).  More rows than SMs: smaller CTAs, two an SM (256 rows of
   // 2000: 69 us against 88).
   const int64_t rows = static_cast<int64_t>(cache->n_seqs) * cache->Hkv;

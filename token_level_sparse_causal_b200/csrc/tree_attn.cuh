@@ -56,7 +56,7 @@ constexpr int TR_MAX_RAW = 5;    // e4m3: tiles of codes, 16 KB, in a ring, at m
 constexpr int TR_OVERHEAD = 3;   // what a unit costs beside its key tiles, in tiles (see tree_split)
 constexpr int TR_SCALES = 8;     // e4m3: key tiles whose scales are held or on their way
 constexpr uint32_t RAW_BYTES = 128u * 128u;
-constexpr int TR_CONV = 256;     // e4m3: converting threads (4 x 131072 tokens, T = 16: 330 us, 128 of them 430)
+constexpr int TR_CONV = 256;     // e4m3: converting threads (4 sequences up to 131072, T = 16: 330 us, 128 of them 430)
 __host__ __device__ constexpr int tr_threads(bool kv8) { return 384 + (kv8 ? TR_CONV : 0); }
 
 // What a call's kernels share: the unit geometry.
