@@ -1,0 +1,66 @@
+"""hs2_cache_weights (through the C ABI) with rows that are not finite, against
+the fp64 oracle: a counted row's NaN reaches the weights of every key that the
+row sees, a row that is left out reaches none.  Finite weights keep the bound
+of test_gpu_tree_attn.py (3e-4 relative)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as so
+from tests import gpu_harness as H
+from tests.serving_cases import Paged, f64
+from token_level_sparse_causal_b200 import hs2
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    H.ensure_built()
+    hs2.hs2_debug_set(H.WAIT_LIMIT_NS, 0)
+
+
+def _collect(c, lse, counted=None):
+    """acc (from zeros) of the kernel and of the oracle."""
+    acc, ab = H.guarded((len(c.ctx), c.Hkv, c.max_pages * c.page), torch.float32, DEV)
+    cnt = None if counted is None else torch.from_numpy(counted).to(DEV)
+    hs2.hs2_cache_weights(c.cache, c.draft, c.d["q"], torch.from_numpy(lse).float().to(DEV), cnt, acc)
+    hs2.hs2_sync()
+    assert H.guards_intact(ab)
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = so.cache_weights(f64(c.q), c.k64, c.table.numpy(), c.page, c.ctx, c.cu, c.masks,
+                               lse.astype(np.float32).astype(np.float64), counted, np.zeros(acc.shape))
+    return acc.double().cpu().numpy(), ref
+
+
+def _close(got, ref):
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    ok = ~np.isnan(ref)
+    assert (np.abs(got[ok] - ref[ok]) <= 3e-4 * ref[ok]).all()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("Hq,drafts", [(1, 64), (2, 40), (8, 12)])
+def test_a_counted_row_that_is_not_finite_reaches_its_keys(Hq, drafts, kv8):
+    """In every column of a chunk of 32, by its log-sum and by its query."""
+    c = Paged([300, 41], [drafts, 2], Hq, 1, kv8, 64, True, seed=50)
+    _, rl, _ = c.oracle()
+    c.device(DEV)
+    for column in range(34):
+        t, h = divmod(column, Hq)
+        lse = rl.copy()
+        lse[h, t] = np.nan
+        got, ref = _collect(c, lse)
+        assert np.isnan(ref[0, 0, :300]).all() and not np.isnan(ref[1]).any()
+        _close(got, ref)
+    for column in range(32):
+        t, h = divmod(column, Hq)
+        q = c.q.clone()
+        c.q[t, h, 7] = float("nan")
+        c.d["q"].copy_(c.q)
+        _close(*_collect(c, rl))
+        c.q = q

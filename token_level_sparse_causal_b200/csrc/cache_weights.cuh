@@ -148,7 +148,7 @@ __device__ __forceinline__ void weights_add(const uint32_t (&sr)[32], uint64_t f
       if (KV8) score = f2_mul(score, i ? f2_pack(qs.z, qs.w) : f2_pack(qs.x, qs.y));
       const uint64_t x = f2_fma(score, f2, i ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y));
       const bool poly = ALL && pair % 4 == 1;
-      sum[pair & 3] = f2_add(sum[pair & 3], poly ? exp2_fma_x2<4>(x) : ex2_x2(x));
+      sum[pair & 3] = f2_add(sum[pair & 3], poly ? exp2_fma_nan_x2<4>(x) : ex2_x2(x));
     }
   }
 }

@@ -111,12 +111,10 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-// exp2_fma3 / exp2_fma4 on a pair, with the arithmetic in f32x2 form.
+// exp2_fma3 / exp2_fma4 on a pair that is -125 or more, with the arithmetic in
+// f32x2 form.
 template <int DEG>
-__device__ __forceinline__ uint64_t exp2_fma_x2(uint64_t xv) {
-  float a, b;
-  f2_unpack(xv, a, b);
-  const uint64_t x = f2_pack(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
+__device__ __forceinline__ uint64_t exp2_fma_above_x2(uint64_t x) {
   const uint64_t magic = f2_pack(12582912.0f, 12582912.0f);
   const uint64_t t = f2_add(x, magic);
   const uint64_t tm = f2_add(t, f2_pack(-12582912.0f, -12582912.0f));
@@ -137,6 +135,29 @@ __device__ __forceinline__ uint64_t exp2_fma_x2(uint64_t xv) {
   f2_unpack(t, t0, t1);
   return f2_pack(__int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)),
                  __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23)));
+}
+
+template <int DEG>
+__device__ __forceinline__ uint64_t exp2_fma_x2(uint64_t xv) {
+  float a, b;
+  f2_unpack(xv, a, b);
+  return exp2_fma_above_x2<DEG>(f2_pack(fmaxf(a, -125.0f), fmaxf(b, -125.0f)));
+}
+
+// The same with a NaN for a NaN (above, fmaxf and the exponent's integer sum
+// turn it into a number): the maximum keeps it, and a last product with zero
+// carries it past the sum.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+template <int DEG>
+__device__ __forceinline__ uint64_t exp2_fma_nan_x2(uint64_t xv) {
+  float a, b;
+  f2_unpack(xv, a, b);
+  const uint64_t x = f2_pack(fmax_nan(a, -125.0f), fmax_nan(b, -125.0f));
+  return f2_fma(x, 0ull, exp2_fma_above_x2<DEG>(x));
 }
 
 __device__ __forceinline__ uint64_t ex2_x2(uint64_t xv) {
