@@ -64,3 +64,30 @@ def test_a_counted_row_that_is_not_finite_reaches_its_keys(Hq, drafts, kv8):
         c.d["q"].copy_(c.q)
         _close(*_collect(c, rl))
         c.q = q
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("Hq,drafts", [(1, 64), (2, 5), (8, 12), (16, 33)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_row_that_is_left_out_reaches_no_key(bad, Hq, drafts, kv8):
+    """By counted = 0 (its log-sum is NaN then, or finite), or by a log-sum of -inf."""
+    c = Paged([300, 41], [drafts, 2], Hq, 1, kv8, 64, True, seed=51)
+    _, rl, _ = c.oracle()
+    out = [1, drafts - 2]
+    for t in out:
+        c.q[t, :, 7] = bad
+        c.q[t, :, 8] = -bad
+    c.device(DEV)
+    counted = np.ones(c.n_tok, np.uint8)
+    counted[out] = 0
+    for lse_of_out in (rl[:, out], np.nan, np.inf):
+        lse = rl.copy()
+        lse[:, out] = lse_of_out
+        got, ref = _collect(c, lse, counted)
+        assert np.isfinite(ref).all()
+        _close(got, ref)
+    lse = rl.copy()
+    lse[:, out] = -np.inf
+    got, ref = _collect(c, lse)
+    assert np.isfinite(ref).all()
+    _close(got, ref)

@@ -131,10 +131,13 @@ struct WeightWalk {
 // Adds 32 columns' weights of one key to sum.  ALL: every column collects, so
 // that some exponentials may leave the MUFU unit (the polynomial has no zero
 // for a column that does not; skipping such columns eight at a time cost more
-// in branches than it saved).
+// in branches than it saved).  Else those of the bits of `live` do: the others'
+// scores may be anything in bf16 (a row that is left out, TMEM behind the rows),
+// an infinity or a NaN too, so they are replaced; e4m3 queries that are left out
+// enter the product as zeros (replacing their scores here took 58 us for 45).
 template <bool KV8, bool ALL>
 __device__ __forceinline__ void weights_add(const uint32_t (&sr)[32], uint64_t f2, const float* nlse,
-                                            const float* qsc, uint64_t (&sum)[4]) {
+                                            const float* qsc, uint32_t live, uint64_t (&sum)[4]) {
   const float4* nl4 = reinterpret_cast<const float4*>(nlse);
   const float4* qs4 = reinterpret_cast<const float4*>(qsc);
 #pragma unroll
@@ -146,7 +149,12 @@ __device__ __forceinline__ void weights_add(const uint32_t (&sr)[32], uint64_t f
       const int c = 4 * e + 2 * i, pair = 2 * e + i;
       uint64_t score = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
       if (KV8) score = f2_mul(score, i ? f2_pack(qs.z, qs.w) : f2_pack(qs.x, qs.y));
-      const uint64_t x = f2_fma(score, f2, i ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y));
+      uint64_t x = f2_fma(score, f2, i ? f2_pack(nl.z, nl.w) : f2_pack(nl.x, nl.y));
+      if (!ALL && !KV8) {
+        float a, b;
+        f2_unpack(x, a, b);
+        x = f2_pack(live >> c & 1u ? a : -INFINITY, live >> (c + 1) & 1u ? b : -INFINITY);
+      }
       const bool poly = ALL && pair % 4 == 1;
       sum[pair & 3] = f2_add(sum[pair & 3], poly ? exp2_fma_nan_x2<4>(x) : ex2_x2(x));
     }
@@ -329,6 +337,12 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       uint64_t* row_bits = reinterpret_cast<uint64_t*>(smem + SM::BITS) + area * QR;
       float* row_nlse = reinterpret_cast<float*>(smem + SM::NLSE) + area * QR;
       uint32_t* live = reinterpret_cast<uint32_t*>(smem + SM::LIVE) + area * (QR / 32);
+      // the log-sum of column c < rows, -inf where it does not collect
+      auto row_lse = [&](int c) {
+        const int64_t row = w.row0 + w.m * p.R + c / p.G;
+        const float l = wp.lse[static_cast<int64_t>(w.g * p.G + c % p.G) * p.n_tok + row];
+        return !wp.counted || wp.counted[row] ? l : -INFINITY;  // both loads under way at once
+      };
       {
         const int c = 128 * half + r;
         uint64_t bits = 0;
@@ -338,8 +352,8 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           const int64_t row = w.row0 + t;
           bits = p.mask ? p.mask[row] : (2ull << t) - 1;
           if (w.T < 64) bits &= (1ull << w.T) - 1;
-          const float l = wp.lse[static_cast<int64_t>(w.g * p.G + c % p.G) * p.n_tok + row];
-          if ((!wp.counted || wp.counted[row]) && l != -INFINITY) nl = -l * 1.44269504088896340736f;
+          const float l = row_lse(c);
+          if (l != -INFINITY) nl = -l * 1.44269504088896340736f;
         }
         row_bits[c] = bits;
         row_nlse[c] = nl;
@@ -351,6 +365,11 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 945)) break;
         uint4 raw[QR / 32];
         load_queries<QR / 32, 16>(p, w.g, w.row0 + w.m * p.R, rows, warp - 4, raw);
+#pragma unroll
+        for (int s = 0; s < QR / 32; ++s) {
+          const int c = 32 * s + 2 * (warp - 4) + (lane >> 4);
+          if (c < rows && row_lse(c) == -INFINITY) raw[s] = make_uint4(0, 0, 0, 0);
+        }
         split_queries<QR / 32, 16, 1>(raw, smem, SM::QHALF, const_cast<float*>(qsc), rows, warp - 4);
         fence_proxy_async_smem();
       }
@@ -401,7 +420,8 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           tmem_ld32(s_tm + c0, sr);
           tmem_ld_wait();
           reg_fence(sr);
-          if (c0 + 32 > rows) {  // columns behind the rows may hold anything
+          const uint32_t collect = live[c];
+          if (KV8 && c0 + 32 > rows) {  // columns behind the rows may hold anything
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (c0 + e >= rows) sr[e] = 0u;
@@ -413,12 +433,12 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
               const bool seen = d < 0 || (in_reach && (row_bits[c0 + e] >> (d & 63) & 1u));
               const float score = __uint_as_float(sr[e]) * (KV8 ? qsc[c0 + e] : 1.f);
               const float y = ex2_approx(fmaf(score, f, row_nlse[c0 + e]));
-              sum[e & 3] = f2_add(sum[e & 3], f2_pack(seen ? y : 0.f, 0.f));
+              sum[e & 3] = f2_add(sum[e & 3], f2_pack(seen && (KV8 || (collect >> e & 1u)) ? y : 0.f, 0.f));
             }
-          } else if (live[c] == 0xffffffffu) {
-            weights_add<KV8, true>(sr, ff, row_nlse + c0, qsc + c0, sum);
+          } else if (collect == 0xffffffffu) {
+            weights_add<KV8, true>(sr, ff, row_nlse + c0, qsc + c0, collect, sum);
           } else {
-            weights_add<KV8, false>(sr, ff, row_nlse + c0, qsc + c0, sum);
+            weights_add<KV8, false>(sr, ff, row_nlse + c0, qsc + c0, collect, sum);
           }
         }
         tc_fence_before();
