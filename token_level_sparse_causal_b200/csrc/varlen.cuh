@@ -63,7 +63,7 @@ struct VarlenBars {
   uint64_t q_full, q_empty;
   uint64_t full_k[FL_STAGES], full_v[FL_STAGES], empty_k[FL_STAGES], empty_v[FL_STAGES];
   uint64_t v_raw[FL_STAGES];  // a V tile landed whose rows behind the sequence are not yet zeroed
-  uint64_t s_full[2], p_ready[2], o_done[2], o_free;
+  uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t item_full[VL_ITEMS], item_empty[VL_ITEMS];
   uint64_t loads_done;  // an item's loads are all under way
   uint64_t next_full;   // an answer to "which index next" has come
@@ -217,7 +217,6 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
       mbar_init(&bars->p_ready[x], 4);
       mbar_init(&bars->o_done[x], 1);
     }
-    mbar_init(&bars->o_free, 8);
     for (int s = 0; s < VL_ITEMS; ++s) {
       mbar_init(&bars->item_full[s], 1);
       mbar_init(&bars->item_empty[s], VL_READERS);
@@ -309,11 +308,6 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) orr[e] = 0u;
-        }
-        if (c == 3) {  // O is in registers: the next item's products may begin
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->o_free);
         }
         uint32_t pk[16];
 #pragma unroll
@@ -470,9 +464,12 @@ __global__ void __launch_bounds__(FL_THREADS, 1)
           commit(&bars->empty_k[u % FL_STAGES]);
           if (n == 1) commit(&bars->q_empty);
         }
-        // the last item's O has been read (waited for at every item, as each
-        // has its phase)
-        if (it > 0 && !(ok = warp_wait(&bars->o_free, (it - 1) & 1, p.limit_ns, abort_flag, 723))) break;
+        // The first product of a tile writes over the last item's O without a
+        // barrier of its own: it waits for P, and the warps of that tile write P
+        // after they have read O.  (A barrier with a phase an item, waited for by
+        // its parity, would not do: a warpgroup without a tile, or with one that
+        // sees no key, is up to two items ahead, so that two phases may end before
+        // this warp looks.)
         for (int j = 0; j < n && ok; ++j) {
           const int tile = u + j, s = tile % FL_STAGES;
           ok = warp_wait(&bars->full_v[s], (tile / FL_STAGES) & 1, p.limit_ns, abort_flag, 724) &&
