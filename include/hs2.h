@@ -423,9 +423,10 @@ int hs2_varlen_attn(const hs2_varlen* shape, const void* q, const void* k, const
  *
  * max_draft: at least every T_b, 1 .. 64.  Hq / Hkv any whole number up to
  * 16.  A sequence whose lengths are negative, above max_draft or above
- * max_pages * page, rows outside [0, n_tok], or a page outside the pools are
- * reported by hs2_sync as HS2_ERR_INDEX; such a sequence (or such an array
- * cu_draft) is skipped, such a page reads as zeros.
+ * max_pages * page, entries of cu_draft that descend or leave [0, n_tok], or a
+ * page outside the pools are reported by hs2_sync as HS2_ERR_INDEX.  Such a
+ * sequence is skipped, with such a cu_draft the call writes nothing, such a
+ * page reads as zeros.
  */
 typedef struct hs2_draft {
   int32_t n_tok, max_draft, Hq, reserved; /* reserved: 0 */

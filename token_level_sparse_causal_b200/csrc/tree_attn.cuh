@@ -119,7 +119,8 @@ struct TreeSmem {
   static_assert(BYTES <= 232448u, "shared memory of one CTA");
 };
 
-// A sequence's lengths; a bad entry counts as no drafted tokens.
+// A sequence's lengths; a bad entry counts as no drafted tokens (tree_split looks
+// at cu_draft as a whole, for sequences that would share rows).
 __device__ __forceinline__ bool tree_seq(const TreeParams& p, int b, int& row0, int& T, int& ctx) {
   const int64_t r0 = p.cu[b], t = static_cast<int64_t>(p.cu[b + 1]) - r0, c = p.ctx[b];
   const bool ok = r0 >= 0 && t >= 0 && t <= p.max_draft && r0 + t <= p.n_tok && c >= 0 && c + t <= p.max_len;
@@ -205,9 +206,12 @@ __device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool
     int row0, T, ctx;
     int64_t cost;
   };
+  bool ascends = true;  // cu_draft, within [0, n_tok]
   auto look = [&](int b) {
     Seq q{0, 0, 0, 0};
     if (b < p.B) {
+      const int r0 = p.cu[b], r1 = p.cu[b + 1];
+      ascends &= r0 >= 0 && r0 <= r1 && r1 <= p.n_tok;
       if (!tree_seq(p, b, q.row0, q.T, q.ctx) && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
       const int mtiles = !units || q.T <= p.R ? 1 : (q.T + p.R - 1) / p.R;
       if (q.T) q.cost = static_cast<int64_t>(((q.ctx + q.T + 127) >> 7) + over) * (p.Hkv * mtiles);
@@ -219,6 +223,9 @@ __device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool
   for (int b = lane + 32; b < p.B; b += 32) total64 += look(b).cost;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total64 += __shfl_xor_sync(0xffffffffu, total64, o);
+  // a sequence that begins before the last one's end: its rows would be two
+  // sequences', written by both, so nothing is done (reported by look)
+  if (!__all_sync(0xffffffffu, ascends)) total64 = 0;
   if (total64 > 0x7fffffff) {  // beyond any cache; no part of it is done
     if (lane == 0 && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
     total64 = 0;
