@@ -443,9 +443,9 @@ typedef struct hs2_draft {
  * have to be finite, those behind it in its last page may be anything.
  * Rows of o outside [cu_draft[0], cu_draft[n_seqs]) are left alone, those of q
  * may hold anything.  o must not overlap an input.  n_tok = 0 does nothing.
- * Over an e4m3 cache a query may enter as the sum of two e4m3 values times a
- * power of two: off by at most 2^-18 of its row's largest number, and exact
- * where it is not below 2^-9 of that (hs2_cache_weights does the same).
+ * Over an e4m3 cache a query may enter as the sum of three e5m2 values times a
+ * power of two: exact where it is not below 2^-23 of its row's largest number,
+ * else off by at most 2^-31 of that (hs2_cache_weights does the same).
  *
  * workspace: hs2_tree_attn_workspace(cache, draft) bytes, 16-byte aligned; it
  * holds no state between calls, but two calls in flight at once (two graphs

@@ -91,3 +91,60 @@ def test_a_row_that_is_left_out_reaches_no_key(bad, Hq, drafts, kv8):
     got, ref = _collect(c, lse)
     assert np.isfinite(ref).all()
     _close(got, ref)
+
+
+def _outlier(kv8, Hq, drafts, large, small, seed):
+    """Queries with one large dimension among small ones, and keys that are small where the queries are large (so
+    that the scores stay ordinary ones while the small dimensions decide)."""
+    c = Paged([600, 41], [drafts, 2], Hq, 1, kv8, 64, True, seed=seed)
+    c.q = (c.q.float() * (small / 1.5)).to(torch.bfloat16)
+    c.q[:, :, 7] = large
+    if kv8:
+        from token_level_sparse_causal_b200 import inputs
+        from oracle import hs2_oracle as orc
+        k = torch.from_numpy(c.k64).clone()
+        k[:, :, 7] *= 2.0 ** -6
+        c.k, c.ks = inputs.quantize_e4m3(k.float().nan_to_num().to(torch.bfloat16))
+        c.k64 = orc.dequantize(inputs.as_u8(c.k), c.ks.numpy())
+    else:
+        c.k[:, :, 7] *= 2.0 ** -6
+        c.k64 = f64(c.k)
+    return c
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("large,small", [(64.0, 0.12), (300.0, 1.5), (1e6, 1.0)])
+@pytest.mark.parametrize("Hq,drafts", [(1, 20), (8, 4), (8, 32)])
+def test_a_large_dimension_costs_the_small_ones_nothing(Hq, drafts, large, small, kv8):
+    """Scores are fp32 sums: 128 roundings of 2^-23 of the products' magnitudes, for a score s beside them 8
+    roundings of 2^-24 of |s| and |lse| (scales, the argument, the stored log-sum); an exponential and the sum of
+    weights add 2^-17 relative (the polynomial 2.6e-6, ex2 and 64 rows' sums less).  A weight below 2^-125 counts as
+    2^-125 (the polynomial's smallest) or as zero, so a position is off by up to 2^-125 a row on top."""
+    c = _outlier(kv8, Hq, drafts, large, small, seed=52 + drafts)
+    _, rl, _ = c.oracle()
+    c.device(DEV)
+    lse = torch.zeros((Hq, c.n_tok), device=DEV)
+    o = torch.empty_like(c.d["q"])
+    hs2.hs2_tree_attn(c.cache, c.draft, c.d["q"], o, lse, c.ws)
+    hs2.hs2_sync()
+    got_l = lse.double().cpu().numpy()
+    got, ref = _collect(c, rl)
+    q64 = f64(c.q)
+    lim = np.zeros(ref.shape)
+    lim_l = np.zeros(rl.shape)
+    for b, ctx in enumerate(c.ctx):
+        t = c.t[b]
+        at = so.rows_of(c.table[b].numpy(), c.page, ctx + t)
+        seen = so.draft_seen(ctx, c.masks[c.cu[b]:c.cu[b + 1]], t)
+        k = c.k64[at, 0]
+        for i in range(t):
+            r = c.cu[b] + i
+            for h in range(Hq):
+                s = k @ q64[r, h] / np.sqrt(128)
+                err = 128 * 2.0 ** -23 * (np.abs(k) @ np.abs(q64[r, h])) / np.sqrt(128) \
+                    + 8 * 2.0 ** -24 * (np.abs(s) + abs(rl[h, r]))
+                p = np.where(seen[i], np.exp(s - rl[h, r]), 0.0)
+                lim[b, 0, :ctx + t] += p * (np.expm1(err) + 2.0 ** -17) + 2.0 ** -125
+                lim_l[h, r] = (p * err).sum() + 2.0 ** -17
+    assert (np.abs(got - ref) <= lim).all(), np.nanmax(np.abs(got - ref) / np.maximum(lim, 1e-300))
+    assert (np.abs(got_l - rl) <= lim_l).all(), np.max(np.abs(got_l - rl) / lim_l)

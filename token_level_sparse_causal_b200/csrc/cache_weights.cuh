@@ -17,11 +17,11 @@
 // mostly waiting); the second hands its sums to the first through shared memory.
 //
 // e4m3: the codes are an operand of the product as they arrive (kind::f8f6f4).
-// A query row times a power of two is the sum of two e4m3 rows (split_queries),
-// so eight products of 32 give the scores that eight of 16 give in bf16; the
+// A query row times a power of two is the sum of three e5m2 rows (split_queries),
+// so twelve products of 32 give the scores that eight of 16 give in bf16; the
 // key's scale and the row's power of two multiply them afterwards.  Turning the
 // codes into bf16 instead took 245 us for 32 tokens (256 rows) over 2 sequences
-// of up to 131072, where this takes 188.
+// of up to 131072, where this takes 204 (two e4m3 parts, which lost bits, 188).
 //
 // Bound by memory at few rows (4 x 32768 tokens of 64/8 heads, 8 rows: bf16 50
 // us, 5.5 TB/s; e4m3 44 us, 3.3 TB/s, there the steps of a tile are longer than
@@ -37,7 +37,7 @@
 namespace hs2 {
 
 constexpr int CW_ROWS = 256;     // query rows of a pass (128: 222 us for 192 with 512 rows of a bf16 cache)
-constexpr int CW_MAX_ITEMS = 8;  // K tiles in the ring, at most
+constexpr int CW_MAX_ITEMS = 7;  // K tiles in the ring, at most
 constexpr int CW_THREADS = 640;  // loads, products, queries and a spare warp; two warpgroups for each tile parity
 
 struct WeightParams {
@@ -66,11 +66,11 @@ static_assert(sizeof(WeightBars) <= 512, "barrier area");
 template <bool KV8>
 struct WeightSmem {
   static constexpr int QR = CW_ROWS;
-  static constexpr int ITEMS = KV8 ? 8 : 4;
+  static constexpr int ITEMS = KV8 ? 7 : 4;
   static_assert(ITEMS <= CW_MAX_ITEMS, "ring");
   static constexpr uint32_t SLOT = KV8 ? RAW_BYTES : TILE_BYTES;
-  static constexpr uint32_t QHALF = QR * 128u;  // half of d in bf16, or one of the two e4m3 parts
-  static constexpr uint32_t ITEM = 2 * QHALF;   // after Q
+  static constexpr uint32_t QPART = QR * 128u;  // half of d in bf16, or one of the three e5m2 parts
+  static constexpr uint32_t ITEM = (KV8 ? 3 : 2) * QPART;  // after Q
   static constexpr uint32_t BAR = ITEM + ITEMS * SLOT;
   // per epilogue warpgroup and segment parity, for each column (query row):
   static constexpr uint32_t BITS = BAR + 512u;                // uint64 [2][2][QR]: the drafted keys it sees
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         if (!(ok = warp_wait(&bars->q_full, seg & 1, p.limit_ns, abort_flag, 921))) break;
         const int rows = min(p.R, w.T - w.m * p.R) * p.G;
         const uint32_t cols = static_cast<uint32_t>((rows + 15) & ~15);
-        const uint32_t idesc = KV8 ? idesc_e4m3_f32(128, static_cast<int>(cols))
+        const uint32_t idesc = KV8 ? idesc_f8_f32(128, static_cast<int>(cols), 0, 1)
                                    : idesc_bf16_f32(128, static_cast<int>(cols), 0, 0);
         const int n = w.n();
         for (int j = 0; j < n; ++j, ++item) {
@@ -281,9 +281,9 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           const uint64_t da = sdesc_sw128(item_base + slot * SM::SLOT, 16, 1024), db = sdesc_sw128(q_base, 16, 1024);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {  // e4m3: the same keys times both parts of the queries
+            for (int kk = 0; kk < (KV8 ? 12 : 8); ++kk) {  // e4m3: the same keys times each part of the queries
               const uint32_t koff = (KV8 ? 0 : (kk >> 2) * HALF_BYTES) + (kk & 3) * 32;
-              const uint32_t qoff = (kk >> 2) * SM::QHALF + (kk & 3) * 32;
+              const uint32_t qoff = (kk >> 2) * SM::QPART + (kk & 3) * 32;
               if (KV8)
                 umma_ss_f8(tmem + x * QR, da + (koff >> 4), db + (qoff >> 4), idesc, kk > 0 ? 1u : 0u);
               else
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         if (seg > 0 && !mbar_wait(&bars->q_empty, (seg - 1) & 1, p.limit_ns, abort_flag, 931)) break;
         mbar_arrive_expect_tx(&bars->q_full, 2 * half);
         tma_load_3d(smem, &tmQ, &bars->q_full, 0, w.g * p.G, w.row0 + w.m * p.R);
-        tma_load_3d(smem + SM::QHALF, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
+        tma_load_3d(smem + SM::QPART, &tmQ, &bars->q_full, 64, w.g * p.G, w.row0 + w.m * p.R);
         ++seg;
       } while (w.next(p));
       wait_done(&bars->q_full, (seg - 1) & 1, p.limit_ns, 932);
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           const int c = 32 * s + 2 * (warp - 4) + (lane >> 4);
           if (c < rows && row_lse(c) == -INFINITY) raw[s] = make_uint4(0, 0, 0, 0);
         }
-        split_queries<QR / 32, 16, 1>(raw, smem, SM::QHALF, const_cast<float*>(qsc), rows, warp - 4);
+        split_queries<QR / 32, 16, 1>(raw, smem, SM::QPART, const_cast<float*>(qsc), rows, warp - 4);
         fence_proxy_async_smem();
       }
       __syncwarp();

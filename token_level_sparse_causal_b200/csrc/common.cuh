@@ -241,10 +241,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_majo
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Instruction descriptor for kind::f8f6f4 with e4m3 A/B (format 0) and fp32
-// accumulation, K-major operands.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// Instruction descriptor for kind::f8f6f4 with fp32 accumulation, K-major
+// operands, each e4m3 (format 0) or e5m2 (format 1).
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, int a_e5m2, int b_e5m2) {
+  return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(b_e5m2) << 10) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -411,8 +412,8 @@ __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
-// The same of e4m3 operands (kind::f8f6f4: 32 of K an instruction), with the
-// descriptor idesc_e4m3_f32.
+// The same of 8-bit operands (kind::f8f6f4: 32 of K an instruction), with the
+// descriptor idesc_f8_f32.
 __device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                            uint32_t accumulate) {
   asm volatile(

@@ -28,6 +28,20 @@ __device__ __forceinline__ uint32_t e4m3x2_from_f32(float lo, float hi) {
   return c;
 }
 
+__device__ __forceinline__ uint32_t e5m2x2_from_f32(float lo, float hi) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+  return c;
+}
+
+// Two e5m2 codes (low byte = first element) -> f16x2; exact.
+__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t two_codes) {
+  uint32_t r;
+  const uint16_t c = static_cast<uint16_t>(two_codes & 0xFFFFu);
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
 // The codes of eight values of a row, e4m3(v / scale), in pairs.
 __device__ __forceinline__ void e4m3_codes(const float (&v)[8], float scale, uint32_t (&c)[4]) {
   if (scale >= 0x1p-90f) {

@@ -34,7 +34,7 @@
 //            f16 it leaves Q and P their whole range), another fetches the
 //            scales; the K scale multiplies the scores, the V scale multiplies
 //            P before its rounding.  Few rows: K's codes are the products'
-//            operand as they are, the queries pairs of e4m3 rows
+//            operand as they are, the queries sums of three e5m2 rows
 //            (split_queries), and only V is converted (4 x 32768 tokens, T = 1:
 //            107 -> 92 us); for a full block the split of 128 rows costs more
 //            than it saves (64 short sequences, T = 6: 52 us, 62 with it).
@@ -107,7 +107,7 @@ struct TreeSmem {
   static constexpr int ITEMS = CODES ? 2 : KV8 ? 3 : BLOCKS > 1 ? 5 : 6;  // CODES: V tiles only
   static constexpr int K8 = CODES ? 3 : 5, V8 = CODES ? 2 : 0;  // rings of codes; else K's and V's in one
   static_assert(ITEMS <= TR_MAX_ITEMS && K8 <= TR_MAX_RAW && V8 <= TR_MAX_RAW, "rings");
-  static constexpr uint32_t ITEM = TILE_BYTES;  // after Q
+  static constexpr uint32_t ITEM = CODES ? 3 * HALF_BYTES : TILE_BYTES;  // after Q: three parts of it, or two halves
   static constexpr uint32_t K8_AT = ITEM + ITEMS * TILE_BYTES;
   static constexpr uint32_t V8_AT = K8_AT + (KV8 ? K8 * RAW_BYTES : 0u);
   static constexpr uint32_t SCALE = V8_AT + V8 * RAW_BYTES;
@@ -371,15 +371,18 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, int g, int64_t
   }
 }
 
-// Those rows as pairs of e4m3 rows (K-major, 128-byte swizzle, the second part
-// `half` bytes behind): a bf16 value has 8 significant bits, two e4m3 values of
-// 4 hold it where it is not below 2^-9 of its row's maximum (then the error is
-// at most 2^-18 of that maximum).  A row is scaled by the power of two that
-// brings its maximum to [128, 256), or less for a row of zeros or nearly so;
-// qsc gets the inverse.  Steps that begin at
-// `upto` or behind are left out; COPIES copies of the tile are written.
+// Those rows as sums of three e5m2 rows (K-major, 128-byte swizzle, the parts
+// `part` bytes apart).  A row is scaled by the power of two that brings its
+// maximum to [2^14, 2^15), or less for a row of zeros or nearly so; qsc gets the
+// inverse.  The first two parts leave at most the last of a bf16 value's 8 bits,
+// so the three are exact where the value is not below 2^-23 of its row's maximum
+// (2^-9 scaled; e5m2's smallest step is 2^-16), else off by at most 2^-31 of it.
+// Two e4m3 parts, which reach down to 2^-9 only, were off by up to 2^-17 of the
+// maximum, and with one large dimension among small ones so were the scores.
+// Steps that begin at `upto` or behind are left out; COPIES copies of the tile
+// are written.
 template <int STEPS, int WARPS, int COPIES>
-__device__ __forceinline__ void split_queries(const uint4 (&raw)[STEPS], uint8_t* smem, uint32_t half, float* qsc,
+__device__ __forceinline__ void split_queries(const uint4 (&raw)[STEPS], uint8_t* smem, uint32_t part, float* qsc,
                                               int upto, int w) {
   const int lane = threadIdx.x & 31, l16 = lane & 15;
   constexpr int STEP = 2 * WARPS;
@@ -393,28 +396,32 @@ __device__ __forceinline__ void split_queries(const uint4 (&raw)[STEPS], uint8_t
     for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7f80u, (v[e] >> 16) & 0x7f80u));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // not below 2^-111: the inverse times log2(e) / sqrt(d) has to stay a normal
+    // not below 2^-104: the inverse times log2(e) / sqrt(d) has to stay a normal
     // number (as a subnormal it became 0, and 0 times a masked key's -inf a NaN)
-    const uint32_t eb = max(top >> 7, 16u);
-    const float up = __uint_as_float((261u - eb) << 23);
-    uint32_t hi[2], lo[2];
+    const uint32_t eb = max(top >> 7, 23u);
+    const float up = __uint_as_float((268u - eb) << 23);
+    uint32_t codes[3][2];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float x = __uint_as_float(v[e] << 16) * up, y = __uint_as_float(v[e] & 0xffff0000u) * up;
-      const uint32_t a = e4m3x2_from_f32(x, y), h = e4m3x2_to_f16x2(a);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      const uint32_t b = e4m3x2_from_f32(x - f.x, y - f.y);
-      hi[e >> 1] = (e & 1) ? hi[e >> 1] | a << 16 : a;
-      lo[e >> 1] = (e & 1) ? lo[e >> 1] | b << 16 : b;
+      float x = __uint_as_float(v[e] << 16) * up, y = __uint_as_float(v[e] & 0xffff0000u) * up;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t a = e5m2x2_from_f32(x, y);
+        codes[i][e >> 1] = (e & 1) ? codes[i][e >> 1] | a << 16 : a;
+        const uint32_t h = e5m2x2_to_f16x2(a);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        x -= f.x;
+        y -= f.y;
+      }
     }
 #pragma unroll
     for (int k = 0; k < COPIES; ++k) {
       uint8_t* dst = smem + k * STEPS * STEP * 128 + sw128_chunk_offset(c, l16 >> 1, 0) + 8 * (l16 & 1);
-      *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(dst + half) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(dst + i * part) = make_uint2(codes[i][0], codes[i][1]);
     }
     // the codes saturate: a row with an infinity or a NaN is made NaN by its scale
-    if (l16 == 0) qsc[c] = __uint_as_float(eb == 255u ? 0x7fffffffu : (eb - 7u) << 23);
+    if (l16 == 0) qsc[c] = __uint_as_float(eb == 255u ? 0x7fffffffu : (eb - 14u) << 23);
   }
 }
 
@@ -821,12 +828,13 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
                                                 : item_base + (u % ITEMS) * TILE_BYTES, 16, 1024);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {  // CODES: the same keys times both parts of the queries
-              const uint32_t step = (kk & 3) * 32 >> 4, second = (kk >> 2) * HALF_BYTES >> 4;
+            for (int kk = 0; kk < (CODES ? 12 : 8); ++kk) {  // CODES: the same keys times each part of the queries
+              const uint32_t step = (kk & 3) * 32 >> 4, part = (kk >> 2) * HALF_BYTES >> 4;
               if (CODES)
-                umma_ss_f8(tmem + x * 128, da + second + step, db + step, idesc_e4m3_f32(128, 128), kk > 0 ? 1u : 0u);
+                umma_ss_f8(tmem + x * 128, da + part + step, db + step, idesc_f8_f32(128, 128, 1, 0),
+                           kk > 0 ? 1u : 0u);
               else
-                umma_ss(tmem + x * 128, da + second + step, db + second + step, IDESC_S, kk > 0 ? 1u : 0u);
+                umma_ss(tmem + x * 128, da + part + step, db + part + step, IDESC_S, kk > 0 ? 1u : 0u);
             }
             umma_commit(&bars->s_full[x]);
             umma_commit(CODES ? &bars->k8_empty[u % K8] : &bars->empty[u % ITEMS]);
@@ -968,7 +976,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       }
     } else {
       // ==== e4m3: codes to bf16, K's and V's or (CODES) V's, and a segment's queries
-      // to pairs of codes
+      // to sums of codes
       TreeWalk w;
       if (KV8 && !(p.flags & FLAG_SKIP_LOADS) && w.begin(p, bars)) {
         const int pt = threadIdx.x - 384;
