@@ -443,6 +443,10 @@ typedef struct hs2_draft {
  * have to be finite, those behind it in its last page may be anything.
  * Rows of o outside [cu_draft[0], cu_draft[n_seqs]) are left alone, those of q
  * may hold anything.  o must not overlap an input.  n_tok = 0 does nothing.
+ * The work of a call, the sum over its sequences of
+ *   (ceil((ctx_len + T) / 128) + 3) * Hkv * ceil(T / floor(128 * Hkv / Hq)),
+ * has to stay below 2^31 (only sequences that share pages can pass that); above
+ * it HS2_ERR_INDEX is reported and nothing is written.
  * Over an e4m3 cache a query may enter as the sum of three e5m2 values times a
  * power of two: exact where it is not below 2^-23 of its row's largest number,
  * else off by at most 2^-31 of that (hs2_cache_weights does the same).

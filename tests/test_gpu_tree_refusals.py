@@ -56,3 +56,23 @@ def test_one_bad_entry_behind_the_first_32_sequences():
     c = Paged([i % 200 for i in range(100)], [1] * 100, 4, 1, False, 16, False, seed=71).device(DEV)
     c.d["cu"][70] = 68
     _writes_nothing(c)
+
+
+def test_more_work_than_a_call_takes():
+    """4096 sequences of 2^20 - 1 tokens (one page, named over and over) and a drafted one, for 64 heads: 2^31 tiles,
+    and three more a unit."""
+    B, H_, pages = 4096, 64, 1 << 13
+    k = torch.zeros((128, H_, 128), dtype=torch.bfloat16, device=DEV)
+    cache = hs2.make_cache(k, k, torch.zeros((B, pages), dtype=torch.int32, device=DEV), 128)
+    q = torch.zeros((B, H_, 128), dtype=torch.bfloat16, device=DEV)
+    cu = torch.arange(B + 1, dtype=torch.int32, device=DEV)
+    draft = hs2.make_draft(q, cu, torch.full((B,), 128 * pages - 1, dtype=torch.int32, device=DEV), None, 1)
+    assert B * H_ * (pages + 3) == 2 ** 31 + 3 * 2 ** 18
+    o = torch.full_like(q, 5.0)
+    lse = torch.full((H_, B), 5.0, device=DEV)
+    ws = torch.empty(hs2.tree_attn_workspace_bytes(cache, draft), dtype=torch.uint8, device=DEV)
+    hs2.hs2_tree_attn(cache, draft, q, o, lse, ws)
+    with pytest.raises(hs2.Hs2Error) as e:
+        hs2.hs2_sync()
+    assert e.value.code == hs2.HS2_ERR_INDEX
+    assert (o == 5).all() and (lse == 5).all()

@@ -226,7 +226,7 @@ __device__ __forceinline__ void tree_split(const TreeParams& p, Bars* bars, bool
   // a sequence that begins before the last one's end: its rows would be two
   // sequences', written by both, so nothing is done (reported by look)
   if (!__all_sync(0xffffffffu, ascends)) total64 = 0;
-  if (total64 > 0x7fffffff) {  // beyond any cache; no part of it is done
+  if (total64 > 0x7fffffff) {  // only by sequences that share pages; no part of it is done
     if (lane == 0 && blockIdx.x == 0) report(HS2_ERR_INDEX, where);
     total64 = 0;
   }
