@@ -102,6 +102,7 @@ static_assert(sizeof(TreeBars) <= TR_BAR_BYTES, "barrier area");
 // RB: rows of a block (32 or 128); a unit has RB / G tokens.
 template <bool KV8, int RB>
 struct TreeSmem {
+  static_assert(RB == 32 || RB == 128, "four blocks or one");
   static constexpr int BLOCKS = 128 / RB;
   static constexpr bool CODES = KV8 && BLOCKS > 1;  // K's codes are the products' operand
   static constexpr int ITEMS = CODES ? 2 : KV8 ? 3 : BLOCKS > 1 ? 5 : 6;  // CODES: V tiles only
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
             return area + static_cast<uint32_t>((taker * (BLOCKS - 1) + giver) * RB + row_r) * (SHARE * 4u);
           };
           auto chunk = [&](int q) {
-            return static_cast<uint32_t>(q ^ ((row_r >> (BLOCKS == 4 ? 2 : 1)) & (SHARE / 4 - 1))) << 4;
+            return static_cast<uint32_t>(q ^ ((row_r >> 2) & (SHARE / 4 - 1))) << 4;
           };
           if (ex > 0 && !(ok = warp_wait(&bars->x_free[x], (ex - 1) & 1, p.limit_ns, abort_flag, 846))) break;
           if (warp_live) {
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->x_ready[x]);
-          if (!(ok = warp_wait(&bars->x_ready[x], ex & 1, p.limit_ns, abort_flag, 847))) break;
+          if (!(ok = warp_wait(&bars->x_ready[x], ex & 1, p.limit_ns, abort_flag, 848))) break;
           if (warp_live) {
             uint64_t mine[SHARE / 2];
 #pragma unroll
@@ -804,9 +805,9 @@ __global__ void __launch_bounds__(tr_threads(KV8), 1)
       } else if (lane == 0 && work) {
         for (int u = max(0, item - ITEMS); u < item; ++u)
           if (raw_used >> (u % ITEMS) & 1u)
-            wait_done(&bars->v_raw[u % ITEMS], ~(raw_uses >> (u % ITEMS)) & 1u, p.limit_ns, 817);
+            wait_done(&bars->v_raw[u % ITEMS], ~(raw_uses >> (u % ITEMS)) & 1u, p.limit_ns, 819);
           else
-            wait_done(&bars->full[u % ITEMS], (u / ITEMS) & 1, p.limit_ns, 814);
+            wait_done(&bars->full[u % ITEMS], (u / ITEMS) & 1, p.limit_ns, 820);
       }
     } else if (warp == 1) {
       // ========================================================== MMA issue

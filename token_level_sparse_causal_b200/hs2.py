@@ -316,7 +316,8 @@ def _strides(t: torch.Tensor) -> tuple:
 
 
 def _rows(t: torch.Tensor, n: int, H: int, what: str, device: int) -> tuple:
-    """Check of a bf16 [n][H][128] tensor with any token and head strides; returns them (see _strides)."""
+    """Type, shape and device of a bf16 [n][H][128] tensor whose last dimension is contiguous (the library checks the
+    other strides); returns its token and head strides (see _strides)."""
     s = t.stride()
     if t.dtype is not torch.bfloat16 or t.shape != (n, H, 128) or s[2] != 1 or t.get_device() != device:
         _need_slow(t, torch.bfloat16, (n, H, 128), what, False, device)
@@ -374,8 +375,9 @@ def make_cache(k, v, page_table, page: int, k_scale=None, v_scale=None) -> Hs2Ca
 
 def hs2_qk_norm_rope(cache: Hs2Cache, q, k, v, q_weight, k_weight, eps: float, inv_freq, positions, slots, q_out,
                      interleaved: bool = False, stream=None) -> None:
-    """q, q_out [n][Hq][128], k, v [n][Hkv][128] bf16 (any token and head strides), inv_freq float64 [rot / 2],
-    positions and slots int32 [n] (slots None: rows 0 .. n - 1 of the pools; -1: no cache write)."""
+    """q, q_out [n][Hq][128], k, v [n][Hkv][128] bf16, inv_freq float64 [rot / 2], positions and slots int32 [n] (slots
+    None: rows 0 .. n - 1 of the pools; -1: no cache write).  Strides are multiples of 8, a head's 128 at least; q's
+    and q_out's heads lie within their token (heads outermost is refused)."""
     n, Hq, _ = q.shape
     dev, Hkv, rot = cache.device, cache.Hkv, 2 * inv_freq.numel()
     qs, outs = _rows(q, n, Hq, "q", dev), _rows(q_out, n, Hq, "q_out", dev)
