@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests import gpu_harness as H
+from tests.serving_cases import f64
 from tests.test_gpu_varlen import _check, _cu, _inputs, _run
 from token_level_sparse_causal_b200 import hs2
 
@@ -44,3 +45,18 @@ def test_many_items_a_cta(kind):
         o, lse, gb = _run(q, k, v, cu_q, cu_k)
         hs2.hs2_sync()
     _check(q, k, v, cu_q, cu_k, o, lse, gb)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(bad):
+    cu = _cu([70, 200, 3])
+    q, k, v = _inputs(cu, cu, 8, 2, seed=61, pad=0)
+    o, lse, _ = _run(q, k, v, cu, None)
+    hs2.hs2_sync()
+    q[100, 5, 7] = bad
+    o2, lse2, gb = _run(q, k, v, cu, None)
+    hs2.hs2_sync()
+    got, ref = f64(o2), f64(o)
+    assert np.isnan(got[100, 5]).all() and torch.isnan(lse2[5, 100])
+    got[100, 5], lse2[5, 100] = ref[100, 5], lse[5, 100]
+    assert np.array_equal(got, ref) and torch.equal(lse, lse2) and all(H.guards_intact(b) for b in gb)
