@@ -468,7 +468,9 @@ int hs2_tree_attn_workspace(const hs2_cache* cache, const hs2_draft* draft, size
  *                   h of g of exp(q_rh . k_j / sqrt(d) - lse[h][r]),
  * with the lse that hs2_tree_attn gave for the same rows.  counted: uint8
  * [n_tok], rows with 0 are left out (drafted tokens that were not accepted);
- * NULL counts all.  Rows with lse = -inf collect nothing.  acc: fp32
+ * NULL counts all.  Rows with lse = -inf collect nothing.  Rows left out may
+ * hold anything; a counted row whose query or lse is NaN makes the weights of
+ * the keys that it sees NaN.  acc: fp32
  * [n_seqs][Hkv][acc_stride]; acc_stride a multiple of 4 and at least every
  * length: a longer sequence is reported as HS2_ERR_INDEX and left out.
  * Positions behind a sequence are not touched.  The sums are added in a fixed

@@ -23,13 +23,13 @@
 // codes into bf16 instead took 245 us for 32 tokens (256 rows) over 2 sequences
 // of up to 131072, where this takes 204 (two e4m3 parts, which lost bits, 188).
 //
-// Bound by memory at few rows (4 x 32768 tokens of 64/8 heads, 8 rows: bf16 50
-// us, 5.5 TB/s; e4m3 44 us, 3.3 TB/s, there the steps of a tile are longer than
-// its load), then by the sums (512 rows: 187 and 223 us), of which the
+// Bound by memory at few rows (4 x 32768 tokens of 64/8 heads, 8 rows: bf16 51
+// us, 5.4 TB/s; e4m3 49 us, 3.0 TB/s, there the steps of a tile are longer than
+// its load), then by the sums (512 rows: 186 and 250 us), of which the
 // exponentials are a large part: 16 a clock and SM on the MUFU unit, so where all
 // 32 columns of a chunk count four of its sixteen pairs take the degree-4
 // polynomial on the FMA pipes instead (2.6e-6; the cubic that kernel (2) mixes in
-// is exact only to 7.5e-5; none of them 199 and 235 us, eight 202 and 257).
+// is exact only to 7.5e-5; none of them 213 and 254 us, eight 204 and 269).
 #pragma once
 
 #include "tree_attn.cuh"
@@ -134,7 +134,7 @@ struct WeightWalk {
 // in branches than it saved).  Else those of the bits of `live` do: the others'
 // scores may be anything in bf16 (a row that is left out, TMEM behind the rows),
 // an infinity or a NaN too, so they are replaced; e4m3 queries that are left out
-// enter the product as zeros (replacing their scores here took 58 us for 45).
+// enter the product as zeros (replacing their scores here took 66 us for 49).
 template <bool KV8, bool ALL>
 __device__ __forceinline__ void weights_add(const uint32_t (&sr)[32], uint64_t f2, const float* nlse,
                                             const float* qsc, uint32_t live, uint64_t (&sum)[4]) {

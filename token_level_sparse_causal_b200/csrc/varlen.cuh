@@ -30,7 +30,7 @@
 //
 // Bound by the tensor cores and the serial chain through the softmax, as
 // kernel (1) is (32/8 heads: one prompt of 32768 tokens 7.9 ms, 1110 TFLOP/s; 32
-// prompts of up to 4096 427 us, 960); short prompts by the latency of a CTA's
+// prompts of up to 4096 425 us, 965); short prompts by the latency of a CTA's
 // few steps (7 of them 12.4 us).
 #pragma once
 
